@@ -59,7 +59,7 @@ typedef enum {
 } tri_status;
 
 /* Flag bits that kernels OR into the workspace flag word. */
-#define TRI_FLAG_ROW_OFFSETS 0x1u /* row_off not non-decreasing from 0 to total_keys */
+#define TRI_FLAG_ROW_OFFSETS 0x1u /* row_off not non-decreasing from 0 to total_keys (or tok_off inconsistent, see tri_append) */
 #define TRI_FLAG_NONFINITE 0x2u   /* a NaN score reached selection (ranked last) */
 #define TRI_FLAG_BLOCK_TABLE 0x4u /* paged: block id out of [0, n_blocks) or row too long for the table; the key is skipped */
 #define TRI_FLAG_STAGE_TIMEOUT 0x8u /* a staged copy of keys did not land within 2 s; the warp that waited skipped its remaining keys */
@@ -136,7 +136,8 @@ const char *tri_status_str(tri_status s);
 
 /* Library version, (major << 16) | minor.  0.2: tri_model carries rope_style and
  * tri_kv_desc elem_type (both zero by default: rotate-half RoPE, bf16).  0.3:
- * calibration files (tri_calib_save / tri_calib_load) and TRI_ERR_IO. */
+ * calibration files (tri_calib_save / tri_calib_load) and TRI_ERR_IO.  0.4: tokens
+ * into the cache and their attention (tri_append, tri_prefill_attention). */
 uint32_t tri_version(void);
 
 /* After a call returned TRI_ERR_CUDA: which CUDA call failed on this thread,
@@ -408,6 +409,91 @@ tri_status tri_decode_attention(const tri_model *m, const tri_kv_desc *kv, const
 tri_status tri_decode_attention_tc(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V,
                                    const void *q, float softmax_scale, float *out, float *lse, void *ws,
                                    size_t ws_bytes, tri_stream_t stream);
+
+/*
+ * New tokens of a batch: the rows of the query, key and value projections, packed
+ * sequence after sequence.
+ *   total_tokens: T >= 0, rows of every token tensor; T may exceed tok_off[n_seqs]
+ *                 (a padded batch): rows from tok_off[n_seqs] on are neither read
+ *                 nor is anything written for them
+ *   tok_off:      device int64 [n_seqs + 1], tok_off[0] = 0, non-decreasing,
+ *                 tok_off[n_seqs] <= T: sequence s's tokens are rows
+ *                 tok_off[s] .. tok_off[s+1]-1, in order
+ *   positions:    device int32 [T], the position each token is rotated to (any
+ *                 int32; usually the tokens seen so far, which exceeds the slots of a
+ *                 compacted cache)
+ *   q, k, v:      bf16, PRE-RoPE, 16-byte aligned: head g of token t of layer l is the
+ *                 d elements from (l * T + t) * stride + g * d (q: n_q_heads heads,
+ *                 k and v: n_kv_heads); the strides, in elements, are multiples of 8
+ *                 and at least heads * d, so the three may be columns of one fused
+ *                 projection.  q may be NULL (keys and values only).
+ */
+typedef struct {
+    int64_t total_tokens;
+    const int64_t *tok_off;
+    const int32_t *positions;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+} tri_token_desc;
+
+/*
+ * Append tokens to the cache (what fills and extends the cache that digest,
+ * 流程详解 steps 2-5, scores, compacts and attends to): queries and keys rotated
+ * by their positions, keys, values and positions written to the tokens' slots.
+ * kv describes the cache WITH the new tokens: sequence s's n_s tokens take the
+ * last n_s slots of each of its rows, token i slot N - n_s + i of a row of N.
+ *   pair f turned by the angle w_f * pos:
+ *     (re, im) -> (re cos - im sin, re sin + im cos),  w_f = rope_theta^(-2f/d)
+ *   key_mode:  TRI_KEYS_POST_ROPE stores turned keys, TRI_KEYS_PRE_ROPE keys as
+ *              given (queries are turned in both)
+ *   q_out:     bf16 [n_layers][T][n_q_heads][d], 16-byte aligned, the turned queries
+ *              (required with tokens->q, else NULL).  May be tokens->q itself where
+ *              q_stride = n_q_heads * d; must not overlap q, k or v otherwise.
+ *   K, V, pos: the cache in kv's layout and element type; pos may be NULL.  Only the
+ *              new tokens' slots are written.
+ *   ws:        at least 256 bytes, 256-byte aligned: only its flag word is used
+ * Angles are reduced exactly in 64-bit fixed-point turns; the rotation is fp32,
+ * rounded once (to nearest even) to the stored type.  fp8 caches saturate: values
+ * beyond +-448 are stored as +-448, NaN as NaN.
+ * A token without a slot (n_s > N) or with inconsistent offsets sets
+ * TRI_FLAG_ROW_OFFSETS, one whose block is out of the pool or table
+ * TRI_FLAG_BLOCK_TABLE; its key, value and position are not stored (its query is
+ * turned all the same).  Slots that two tokens share (a block listed twice) hold
+ * one of them, unspecified which, element by element.
+ */
+tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token_desc *tokens, int32_t key_mode,
+                      void *q_out, void *K, void *V, int32_t *pos, void *ws, size_t ws_bytes, tri_stream_t stream);
+
+/*
+ * Causal attention of a batch of new tokens over the cache that holds them: whole
+ * prompts, prompt chunks behind a cached (or compacted) prefix, a few drafted
+ * tokens, or single tokens, packed with different lengths.  For layer l, sequence s
+ * with n tokens, query head g (KV head h = g / G) and row (l, s, h) of N slots,
+ * token i sees slots j <= N - n + i:
+ *   s_j = softmax_scale * (q . k_j),
+ *   out = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = log sum_j e^{s_j}
+ * (out = 0 and lse = -inf where a token sees no slot).  Slots outside the row and
+ * behind a token do not reach its result, whatever bits they hold.
+ *   kv, K, V:  the cache with the tokens appended (tri_append), either layout and
+ *              element type, 16-byte aligned
+ *   q:         bf16 [n_layers][T][n_q_heads][d], RoPE'd (tri_append's q_out),
+ *              16-byte aligned
+ *   tok_off, total_tokens: as in tri_token_desc
+ *   softmax_scale: finite, > 0
+ *   out:       bf16 [n_layers][T][n_q_heads][d], 16-byte aligned
+ *   lse:       float [n_layers][T][n_q_heads] or NULL
+ *   ws:        tri_prefill_attention_ws_size bytes, 256-byte aligned; first word is
+ *              a flag word (TRI_FLAG_ROW_OFFSETS, also for inconsistent tok_off;
+ *              TRI_FLAG_BLOCK_TABLE: that key is skipped).  Calls that may run at the
+ *              same time need a workspace each.
+ * Scores, softmax statistics and sums are fp32; the weights e^{s_j - max} enter the
+ * product with V as bf16.  Rows of out and lse from tok_off[n_seqs] on are left as
+ * they were.
+ */
+size_t tri_prefill_attention_ws_size(const tri_model *m, int32_t n_seqs, int64_t total_tokens);
+tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V, const void *q,
+                                 const int64_t *tok_off, int64_t total_tokens, float softmax_scale, void *out,
+                                 float *lse, void *ws, size_t ws_bytes, tri_stream_t stream);
 
 /*
  * tri_score without a workspace argument, for callers that cannot allocate

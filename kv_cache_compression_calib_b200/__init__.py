@@ -21,7 +21,7 @@ from . import _abi
 from ._abi import (TRI_ELEM_BF16, TRI_ELEM_FP8_E4M3, TRI_FLAG_BLOCK_TABLE,  # noqa: F401
                    TRI_FLAG_NONFINITE, TRI_FLAG_ROW_OFFSETS, TRI_FLAG_STAGE_TIMEOUT,
                    TRI_KEYS_POST_ROPE, TRI_KEYS_PRE_ROPE, TRI_KV_CONTIG, TRI_KV_PAGED,
-                   TRI_MAX_OFFSETS, TRI_ROPE_HALF, TRI_ROPE_INTERLEAVED, TriKvDesc, TriModel, TriOutDesc)
+                   TRI_MAX_OFFSETS, TRI_ROPE_HALF, TRI_ROPE_INTERLEAVED, TriKvDesc, TriModel, TriOutDesc, TriTokenDesc)
 
 _L = _abi.load()
 
@@ -129,6 +129,37 @@ def out_paged(block_table: torch.Tensor, block_size: int, n_blocks: int) -> TriO
     d = TriOutDesc(TRI_KV_PAGED, block_table.shape[1], _p(block_table).value, block_size, 0,
                    int(n_blocks))
     d._keep = (block_table,)
+    return d
+
+
+def _token_rows(t: torch.Tensor, what: str):
+    """A [T][heads][d] (one layer) or [L][T][heads][d] bf16 tensor whose heads are dense: (pointer, elements
+    from one token's row to the next)."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor, got one on {t.device}")
+    if t.dtype != torch.bfloat16 or t.dim() not in (3, 4):
+        raise ValueError(f"{what}: expected a bf16 tensor [T][heads][d] or [L][T][heads][d]")
+    st, sh = t.stride(), t.shape
+    if t.numel() == 0:
+        return t.data_ptr(), sh[-2] * sh[-1]
+    row = st[-3] if sh[-3] > 1 else (st[0] if t.dim() == 4 and sh[0] > 1 else sh[-2] * sh[-1])
+    if st[-1] != 1 or (sh[-2] > 1 and st[-2] != sh[-1]) or (t.dim() == 4 and sh[0] > 1 and st[0] != sh[1] * row):
+        raise ValueError(f"{what}: heads must be dense and tokens evenly spaced (call .contiguous())")
+    return t.data_ptr(), row
+
+
+def tokens(k: torch.Tensor, v: torch.Tensor, tok_off: torch.Tensor, positions: torch.Tensor, q=None) -> TriTokenDesc:
+    """New tokens for ``tri_append``: pre-RoPE ``q``/``k``/``v`` bf16 [L][T][heads][d] (or [T][heads][d] for one
+    layer; they may be column slices of one fused projection), ``tok_off`` int64 [S+1], ``positions`` int32 [T]."""
+    T = k.shape[-3]
+    if k.shape != v.shape or positions.shape != (T,) or (q is not None and q.shape[:-2] != k.shape[:-2]):
+        raise ValueError("tokens: q, k, v and positions disagree on the number of tokens, layers or heads")
+    if tok_off.dtype != torch.int64 or positions.dtype != torch.int32:
+        raise ValueError("tokens: tok_off must be int64 and positions int32")
+    (kp, ks), (vp, vs) = _token_rows(k, "k"), _token_rows(v, "v")
+    qp, qs = _token_rows(q, "q") if q is not None else (None, 0)
+    d = TriTokenDesc(T, _p(tok_off).value, _p(positions).value, qp, kp, vp, qs, ks, vs)
+    d._keep = (q, k, v, tok_off, positions)
     return d
 
 
@@ -243,6 +274,74 @@ def tri_decode_attention_tc(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torc
     _check(_L.tri_decode_attention_tc(ctypes.byref(m), ctypes.byref(kv), _p(K), _p(V), _p(q), float(softmax_scale),
                                       _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size(), _s(stream)),
            "tri_decode_attention_tc")
+
+
+def _same_device(*ts) -> None:
+    """Kernels are launched on the current device: every tensor has to live there."""
+    cur = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"a tensor on {t.device} in a call on cuda:{cur} (use torch.cuda.device)")
+
+
+def _sized(t, n: int, dtype, what: str) -> None:
+    if t.numel() != n or t.dtype != dtype:
+        raise ValueError(f"{what}: expected {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
+
+
+def alloc_append_workspace(device=None, stream=None) -> torch.Tensor:
+    """The flag word ``tri_append`` reports anomalies in (read with ``tri_status_check``)."""
+    ws = torch.empty(256, dtype=torch.uint8, device=device or "cuda")
+    tri_workspace_init(ws, stream)
+    return ws
+
+
+def tri_append(m: TriModel, kv: TriKvDesc, tokens: TriTokenDesc, key_mode: int, q_out, K: torch.Tensor,
+               V: torch.Tensor, pos, ws: torch.Tensor, stream=None) -> None:
+    """Rotate new tokens' queries and keys by their positions; write keys, values and positions to the last slots
+    of the rows ``kv`` describes.  ``q_out`` bf16 [L][T][Hq][d] (None when the tokens have no q)."""
+    q, k = tokens._keep[:2]
+    L, T = m.n_layers, tokens.total_tokens
+    _sized(k, L * T * m.n_kv_heads * m.head_dim, torch.bfloat16, "k")
+    if q is not None:
+        _sized(q, L * T * m.n_q_heads * m.head_dim, torch.bfloat16, "q")
+    if q_out is not None:
+        _sized(q_out, L * T * m.n_q_heads * m.head_dim, torch.bfloat16, "q_out")
+    _same_device(k, q_out, K, V, pos, ws)
+    _check(_L.tri_append(ctypes.byref(m), ctypes.byref(kv), ctypes.byref(tokens), int(key_mode), _p(q_out), _p(K),
+                         _p(V), _p(pos), _p(ws), ws.numel() * ws.element_size(), _s(stream)), "tri_append")
+
+
+def tri_prefill_attention_ws_size(m: TriModel, n_seqs: int, total_tokens: int) -> int:
+    return int(_L.tri_prefill_attention_ws_size(ctypes.byref(m), int(n_seqs), int(total_tokens)))
+
+
+def alloc_prefill_attention_workspace(m: TriModel, n_seqs: int, total_tokens: int, device=None,
+                                      stream=None) -> torch.Tensor:
+    n = tri_prefill_attention_ws_size(m, n_seqs, total_tokens)
+    if n == 0:
+        raise TriError(_abi.TRI_ERR_INVALID_ARG, "tri_prefill_attention_ws_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    tri_workspace_init(ws, stream)
+    return ws
+
+
+def tri_prefill_attention(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.Tensor, q: torch.Tensor,
+                          tok_off: torch.Tensor, softmax_scale: float, out: torch.Tensor, lse, ws: torch.Tensor,
+                          stream=None) -> None:
+    """Causal softmax attention of the appended tokens' queries ``q`` bf16 [L][T][Hq][d] over the cache rows that
+    end with them -> ``out`` bf16 [L][T][Hq][d], ``lse`` float [L][T][Hq] or None."""
+    rows = m.n_layers * m.n_q_heads * m.head_dim
+    T = q.numel() // rows
+    _sized(q, T * rows, torch.bfloat16, "q")
+    _sized(out, T * rows, torch.bfloat16, "out")
+    _sized(tok_off, kv.n_seqs + 1, torch.int64, "tok_off")
+    if lse is not None:
+        _sized(lse, T * m.n_layers * m.n_q_heads, torch.float32, "lse")
+    _same_device(K, V, q, tok_off, out, lse, ws)
+    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _p(K), _p(V), _p(q), _p(tok_off), T,
+                                    float(softmax_scale), _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size(),
+                                    _s(stream)), "tri_prefill_attention")
 
 
 def tri_score_compact(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.Tensor, pos, centres: torch.Tensor,

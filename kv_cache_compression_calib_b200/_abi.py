@@ -36,7 +36,8 @@ EXPORTS = ("tri_status_str", "tri_version", "tri_last_error", "tri_workspace_siz
            "tri_score", "tri_compact", "tri_status_check", "tri_score_noalloc", "tri_calib_update",
            "tri_calib_stats", "tri_key_centres_ws_size", "tri_key_centres", "tri_attention_ws_size",
            "tri_decode_attention", "tri_score_compact", "tri_selftest_wait_timeout", "tri_calib_save",
-           "tri_calib_load", "tri_decode_attention_tc")
+           "tri_calib_load", "tri_decode_attention_tc", "tri_append", "tri_prefill_attention_ws_size",
+           "tri_prefill_attention")
 TRI_FUSED_MAX_ROW = 32768
 TRI_FUSED_PREFER_ROW = 8192
 TRI_NOALLOC_MAX_ROWS = 4096
@@ -62,6 +63,13 @@ class TriOutDesc(ctypes.Structure):
     _fields_ = [("layout", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p), ("block_size", ctypes.c_int32),
                 ("pad_", ctypes.c_int32), ("n_blocks", ctypes.c_int64)]
+
+
+class TriTokenDesc(ctypes.Structure):
+    _fields_ = [("total_tokens", ctypes.c_int64), ("tok_off", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -104,6 +112,14 @@ def load(path: str = LIB_PATH):
                                        ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]
     L.tri_decode_attention_tc.restype = ctypes.c_int
     L.tri_decode_attention_tc.argtypes = L.tri_decode_attention.argtypes
+    L.tri_append.restype = ctypes.c_int
+    L.tri_append.argtypes = [ctypes.POINTER(TriModel), ctypes.POINTER(TriKvDesc), ctypes.POINTER(TriTokenDesc),
+                             ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+    L.tri_prefill_attention_ws_size.restype = ctypes.c_size_t
+    L.tri_prefill_attention_ws_size.argtypes = [ctypes.POINTER(TriModel), ctypes.c_int32, ctypes.c_int64]
+    L.tri_prefill_attention.restype = ctypes.c_int
+    L.tri_prefill_attention.argtypes = [ctypes.POINTER(TriModel), ctypes.POINTER(TriKvDesc), _P, _P, _P, _P,
+                                        ctypes.c_int64, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]
     L.tri_key_centres_ws_size.restype = ctypes.c_size_t
     L.tri_key_centres_ws_size.argtypes = [ctypes.POINTER(TriModel), ctypes.c_int32]
     L.tri_key_centres.restype = ctypes.c_int

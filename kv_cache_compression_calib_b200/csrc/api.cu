@@ -116,7 +116,7 @@ const char *tri_status_str(tri_status s) {
     return "TRI_ERR_UNKNOWN";
 }
 
-uint32_t tri_version(void) { return (0u << 16) | 3u; }
+uint32_t tri_version(void) { return (0u << 16) | 4u; }
 
 const char *tri_last_error(void) { return g_last_error; }
 
@@ -504,6 +504,108 @@ tri_status tri_decode_attention_tc(const tri_model *m, const tri_kv_desc *kv, co
     const cudaError_t e = launch_attention_tc(p, R, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported) return TRI_ERR_UNSUPPORTED;
     return cuda_status(e, "tensor-memory attention kernel launch");
+}
+
+tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token_desc *tokens, int32_t key_mode,
+                      void *q_out, void *K, void *V, int32_t *pos, void *ws, size_t ws_bytes, tri_stream_t stream) {
+    tri_status st = check_model(m);
+    if (st != TRI_OK) return st;
+    Geometry geo;
+    if ((st = check_kv(m, kv, &geo)) != TRI_OK) return st;
+    if (!tokens || tokens->total_tokens < 0) return TRI_ERR_INVALID_ARG;
+    if (key_mode != TRI_KEYS_POST_ROPE && key_mode != TRI_KEYS_PRE_ROPE) return TRI_ERR_INVALID_ARG;
+    if ((st = check_ws(ws, ws_bytes, 256)) != TRI_OK) return st;
+    const int64_t T = tokens->total_tokens, L = m->n_layers, D = m->head_dim;
+    if (T == 0) return TRI_OK;
+    if (!tokens->tok_off || !tokens->positions || !tokens->k || !tokens->v || !K || !V || K == V ||
+        (tokens->q == nullptr) != (q_out == nullptr))
+        return TRI_ERR_INVALID_ARG;
+    if (T > (1LL << 31) - 1 || L * T > (1LL << 40) || m->n_q_heads > (1 << 20)) return TRI_ERR_UNSUPPORTED;
+    const int64_t most = 1LL << 40;  // strides beyond this could pass 64-bit byte offsets
+    if (tokens->k_stride < m->n_kv_heads * D || tokens->v_stride < m->n_kv_heads * D || tokens->k_stride > most ||
+        tokens->v_stride > most || (tokens->q && (tokens->q_stride < m->n_q_heads * D || tokens->q_stride > most)))
+        return TRI_ERR_INVALID_ARG;
+    if (!aligned(tokens->k, 16) || !aligned(tokens->v, 16) || !aligned(K, 16) || !aligned(V, 16) ||
+        tokens->k_stride % 8 || tokens->v_stride % 8 || !aligned(tokens->tok_off, 8) || !aligned(tokens->positions, 4) ||
+        (pos && !aligned(pos, 4)) ||
+        (tokens->q && (!aligned(tokens->q, 16) || tokens->q_stride % 8 || !aligned(q_out, 16))))
+        return TRI_ERR_ALIGNMENT;
+    if (q_out) {
+        // Rows [first token's first element, last token's last element] of each input.
+        const auto meets = [&](const void *x, int64_t stride, int64_t width) {
+            const char *a = (const char *)x, *b = a + 2 * ((L * T - 1) * stride + width);
+            const char *o = (const char *)q_out;
+            return o < b && a < o + 2 * L * T * m->n_q_heads * D;
+        };
+        const bool in_place = q_out == tokens->q && tokens->q_stride == m->n_q_heads * D;
+        if ((!in_place && meets(tokens->q, tokens->q_stride, m->n_q_heads * D)) ||
+            meets(tokens->k, tokens->k_stride, m->n_kv_heads * D) || meets(tokens->v, tokens->v_stride, m->n_kv_heads * D))
+            return TRI_ERR_INVALID_ARG;
+    }
+    AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.geo = geo;
+    p.T = T;
+    p.tok_off = tokens->tok_off;
+    p.positions = tokens->positions;
+    p.q = (const char *)tokens->q;
+    p.k = (const char *)tokens->k;
+    p.v = (const char *)tokens->v;
+    p.q_stride = 2 * tokens->q_stride;
+    p.k_stride = 2 * tokens->k_stride;
+    p.v_stride = 2 * tokens->v_stride;
+    p.rotate_keys = key_mode == TRI_KEYS_POST_ROPE;
+    p.q_out = (char *)q_out;
+    p.K = (char *)K;
+    p.V = (char *)V;
+    p.pos = pos;
+    p.flags = (unsigned *)((char *)ws + kWsFlags);
+    // w_f / 2 pi = theta^(-2f/d) / 2 pi as 0.64 fixed-point turns: powers of theta^(-2/d) in
+    // extended precision (relative error below f * 2^-63, so below 2^-24 of a turn at any int32 position).
+    const long double step = powl((long double)m->rope_theta, -2.0L / (long double)D);
+    long double w = 18446744073709551616.0L / 6.283185307179586476925286766559L;
+    for (int f = 0; f < D / 2; f++, w *= step) p.turns[f] = (unsigned long long)w;
+    return cuda_status(launch_append(p, (cudaStream_t)stream), "append_kernel launch");
+}
+
+size_t tri_prefill_attention_ws_size(const tri_model *m, int32_t n_seqs, int64_t total_tokens) {
+    if (check_model(m) != TRI_OK || n_seqs < 1 || total_tokens < 0) return 0;
+    return 256 + ((prefill_scratch_bytes(m->n_layers, n_seqs, m->n_kv_heads, m->n_q_heads / m->n_kv_heads, m->head_dim,
+                                         total_tokens) +
+                   255) &
+                  ~size_t(255));
+}
+
+tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V, const void *q,
+                                 const int64_t *tok_off, int64_t total_tokens, float softmax_scale, void *out,
+                                 float *lse, void *ws, size_t ws_bytes, tri_stream_t stream) {
+    tri_status st = check_model(m);
+    if (st != TRI_OK) return st;
+    Geometry geo;
+    if ((st = check_kv(m, kv, &geo)) != TRI_OK) return st;
+    if (total_tokens < 0 || !std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return TRI_ERR_INVALID_ARG;
+    if ((st = check_ws(ws, ws_bytes, tri_prefill_attention_ws_size(m, kv->n_seqs, total_tokens))) != TRI_OK) return st;
+    if (total_tokens == 0) return TRI_OK;
+    if (!K || !V || !q || !tok_off || !out || out == q) return TRI_ERR_INVALID_ARG;
+    if (total_tokens > (1LL << 31) - 1 || m->n_layers * total_tokens > (1LL << 40) || m->n_q_heads > (1 << 20))
+        return TRI_ERR_UNSUPPORTED;
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(tok_off, 8) ||
+        (lse && !aligned(lse, 4)))
+        return TRI_ERR_ALIGNMENT;
+    PrefillParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.geo = geo;
+    p.T = total_tokens;
+    p.tok_off = tok_off;
+    p.K = (const char *)K;
+    p.V = (const char *)V;
+    p.q = (const uint16_t *)q;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.out = (uint16_t *)out;
+    p.lse = lse;
+    p.part = (float *)((char *)ws + 256);
+    p.flags = (unsigned *)((char *)ws + kWsFlags);
+    return cuda_status(launch_prefill(p, (cudaStream_t)stream), "prefill attention kernel launch");
 }
 
 tri_status tri_status_check(void *ws, uint32_t *flags, tri_stream_t stream) {

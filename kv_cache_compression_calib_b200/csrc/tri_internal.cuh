@@ -141,6 +141,34 @@ struct AttnParams {
     unsigned *flags;
 };
 
+struct AppendParams {
+    Geometry geo;  // the cache with the new tokens in it
+    int64_t T;     // rows of the token tensors
+    const int64_t *tok_off;
+    const int32_t *positions;
+    const char *q, *k, *v;             // bf16, pre-RoPE; q may be null
+    int64_t q_stride, k_stride, v_stride;  // bytes from token to token
+    int32_t rotate_keys;
+    char *q_out, *K, *V;
+    int32_t *pos;  // may be null
+    unsigned *flags;
+    int32_t tile;  // tokens per block step, set at launch
+    unsigned long long turns[128];  // w_f / 2 pi in 0.64 fixed point
+};
+
+struct PrefillParams {
+    Geometry geo;  // the cache with the new tokens in it
+    int64_t T;
+    const int64_t *tok_off;
+    const char *K, *V;
+    const uint16_t *q;  // bf16 [L][T][Hq][D], RoPE'd
+    float scale_log2;   // softmax scale * log2(e)
+    uint16_t *out;      // bf16 [L][T][Hq][D]
+    float *lse;         // [L][T][Hq] or null
+    float *part;        // scratch of split rows
+    unsigned *flags;
+};
+
 constexpr int kFusedMaxRow = TRI_FUSED_MAX_ROW;  // longest row the fused score-and-select kernel holds on chip
 
 struct FusedParams {
@@ -155,6 +183,9 @@ cudaError_t launch_calib(const CalibParams &p, cudaStream_t s);
 cudaError_t launch_fused(const FusedParams &p, int pre_rope, cudaStream_t s);
 cudaError_t launch_attention(const AttnParams &p, cudaStream_t s);
 cudaError_t launch_attention_tc(const AttnParams &p, int64_t R, cudaStream_t s);  // cudaErrorNotSupported outside its case
+cudaError_t launch_append(const AppendParams &p, cudaStream_t s);
+cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s);
+size_t prefill_scratch_bytes(int64_t L, int64_t S, int64_t H, int64_t G, int D, int64_t T);
 cudaError_t launch_calib_update(const CalibUpdateParams &p, cudaStream_t s);
 cudaError_t launch_stats(const StatsParams &p, cudaStream_t s);
 cudaError_t launch_key_centres(const KeyCentreParams &p, cudaStream_t s);

@@ -1,0 +1,101 @@
+"""Host checks of tri_append and tri_prefill_attention: every refusal comes before any
+CUDA call, so these run without a GPU (the addresses are never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+import kv_cache_compression_calib_b200 as tri
+from kv_cache_compression_calib_b200 import _abi
+
+A = 1 << 20
+M = tri.model(1, 32, 8, 1e6)
+BAD, UNSUP, ALIGN, SMALL = (_abi.TRI_ERR_INVALID_ARG, _abi.TRI_ERR_UNSUPPORTED, _abi.TRI_ERR_ALIGNMENT,
+                            _abi.TRI_ERR_WORKSPACE_TOO_SMALL)
+
+
+def kv(layout=0, n_seqs=1, total=4096, row_off=A, table=None, max_blocks=0, bs=0, nb=0, elem=0):
+    return _abi.TriKvDesc(layout, n_seqs, total, row_off, table, max_blocks, bs, nb, elem, 0)
+
+
+def append(m=M, kv_=None, T=4, tok_off=A, positions=A, q=16 * A, k=32 * A, v=48 * A, qs=32 * 128, ks=8 * 128, vs=8 * 128,
+           mode=0, q_out=64 * A, K=80 * A, V=96 * A, pos=None, ws=A, ws_bytes=256, toks=True):
+    t = _abi.TriTokenDesc(T, tok_off, positions, q, k, v, qs, ks, vs)
+    return _abi.load().tri_append(ctypes.byref(m), ctypes.byref(kv_ or kv()), ctypes.byref(t) if toks else None, mode, q_out,
+                                  K, V, pos, ws, ws_bytes, None)
+
+
+def prefill(m=M, kv_=None, K=A, V=2 * A, q=3 * A, tok_off=A, T=4, scale=0.1, out=5 * A, lse=None, ws=A, ws_bytes=1 << 40):
+    return _abi.load().tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv_ or kv()), K, V, q, tok_off, T, scale, out, lse,
+                                             ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(toks=False), BAD), (dict(T=-1), BAD), (dict(tok_off=None), BAD), (dict(positions=None), BAD), (dict(k=None), BAD),
+    (dict(v=None), BAD), (dict(q=None), BAD), (dict(q_out=None), BAD), (dict(K=None), BAD), (dict(V=None), BAD),
+    (dict(V=80 * A), BAD), (dict(mode=2), BAD), (dict(ws=None), BAD), (dict(ws_bytes=255), SMALL), (dict(ws=A + 64), ALIGN),
+    (dict(T=1 << 31), UNSUP), (dict(qs=32 * 128 - 8), BAD), (dict(ks=8 * 128 - 8), BAD), (dict(vs=0), BAD),
+    (dict(ks=-8 * 128), BAD), (dict(qs=1 << 41), BAD), (dict(qs=32 * 128 + 4), ALIGN), (dict(ks=8 * 128 + 2), ALIGN),
+    (dict(q=16 * A + 2), ALIGN), (dict(k=32 * A + 8), ALIGN), (dict(q_out=64 * A + 8), ALIGN), (dict(K=80 * A + 8), ALIGN),
+    (dict(V=96 * A + 2), ALIGN), (dict(tok_off=A + 4), ALIGN), (dict(positions=A + 2), ALIGN), (dict(pos=A + 1), ALIGN),
+    # q_out over the queries (but not exactly in place), over the keys, over the values
+    (dict(q_out=16 * A, qs=48 * 128), BAD), (dict(q_out=16 * A + 16), BAD), (dict(q_out=32 * A), BAD), (dict(q_out=48 * A), BAD),
+    (dict(m=tri.model(1, 32, 8, 1e6, head_dim=96)), UNSUP), (dict(m=tri.model(1, 1 << 21, 8, 1e6), qs=1 << 28), UNSUP),
+    (dict(kv_=kv(n_seqs=0)), BAD), (dict(kv_=kv(elem=3)), BAD), (dict(kv_=kv(layout=1, table=A, max_blocks=2, bs=12, nb=3)), UNSUP),
+])
+def test_append_refuses(kw, status):
+    assert append(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(K=None), BAD), (dict(V=None), BAD), (dict(q=None), BAD), (dict(tok_off=None), BAD), (dict(out=None), BAD),
+    (dict(out=3 * A), BAD), (dict(T=-1), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD), (dict(scale=float("nan")), BAD),
+    (dict(scale=float("inf")), BAD), (dict(K=A + 8), ALIGN), (dict(V=A + 8), ALIGN), (dict(q=A + 8), ALIGN), (dict(out=A + 4), ALIGN),
+    (dict(tok_off=A + 4), ALIGN), (dict(lse=A + 2), ALIGN), (dict(ws=A + 16), ALIGN), (dict(ws=None), BAD), (dict(ws_bytes=255), SMALL),
+    (dict(T=1 << 31), UNSUP), (dict(m=tri.model(1, 32, 8, 1e6, head_dim=32)), UNSUP), (dict(kv_=kv(total=-1)), BAD),
+    (dict(kv_=kv(layout=1)), BAD),
+])
+def test_prefill_refuses(kw, status):
+    assert prefill(**kw) == status
+
+
+def test_no_tokens_is_no_work():
+    assert append(T=0, q=None, q_out=None, k=None, v=None, K=None, V=None, tok_off=None, positions=None) == 0
+    assert prefill(T=0, K=None, V=None, q=None, out=None, tok_off=None) == 0
+
+
+def test_prefill_workspace_size():
+    n = tri.tri_prefill_attention_ws_size
+    assert n(M, 1, 0) >= 256 and n(M, 0, 4) == 0 and n(M, 1, -1) == 0
+    assert n(tri.model(1, 32, 8, 1e6, head_dim=80), 1, 4) == 0
+    for m in (M, tri.model(64, 64, 8, 1e6), tri.model(1, 8, 8, 1e4, head_dim=256)):
+        for S, T in ((1, 1), (16, 16), (3, 5000), (64, 100000)):
+            assert 256 <= n(m, S, T) <= 256 << 20 and n(m, S, T) % 256 == 0
+
+
+class _Fake:
+    """A CUDA tensor as far as tokens() looks at one (there is no device here)."""
+    is_cuda, device, dtype = True, "cuda:0", torch.bfloat16
+
+    def __init__(self, t):
+        self.t = t
+        self.shape, self.numel, self.stride, self.dim = t.shape, t.numel, t.stride, t.dim
+
+    def data_ptr(self):
+        return 64 + 2 * self.t.storage_offset()
+
+
+def test_token_rows_of_fused_projections():
+    x = torch.zeros(3, 5, 10, 64, dtype=torch.bfloat16)
+    rows = lambda t: tri._token_rows(_Fake(t), "x")  # noqa: E731
+    assert rows(x) == (64, 640)
+    assert rows(x[:, :, 4:6]) == (64 + 2 * 4 * 64, 640)
+    assert rows(x[1, :, 4:6])[1] == 640
+    assert rows(x[:, :1, 4:6].contiguous())[1] == 128
+    for bad in (x.transpose(2, 3), x.transpose(0, 1), x[..., ::2], x[:, :, ::2], x[:, :4]):
+        with pytest.raises(ValueError):
+            rows(bad)
+    with pytest.raises(ValueError):
+        tri._token_rows(x, "x")  # not on a GPU
+    with pytest.raises(ValueError):
+        tri._token_rows(_Fake(x[0, 0]), "x")
