@@ -4,93 +4,822 @@
 // row (l, s, h),
 //   s_j = scale * (q . k_j),  out = sum_j e^{s_j} v_j / sum_j e^{s_j},  lse = log sum_j e^{s_j}.
 //
-// One warp per (token, head): each lane holds d/32 dims of the query, a key's dot
-// product is a warp sum, softmax online in base 2 with fp32 statistics.
+// 4 d flops per visible (query, key) pair: tensor-core bound for prompts, HBM bound
+// (K and V read once) for a few tokens over a long row.  The G query heads of a KV
+// head share its keys, so a block's rows are the (token, head) pairs of one KV head in
+// token order: a prompt of n tokens is n * G rows, cut into blocks of up to 256.
+//
+// A block (one per SM, 16 warps) computes, for its two 128-row query tiles,
+//   S = Q K^T  and  O += P V,  P = 2^(S scale log2(e) - m),
+// on tcgen05.mma (kind::f16, bf16 operands, fp32 accumulators in tensor memory):
+//   - warps 0-3 and 4-7: the softmax of query tile 0 and 1, one thread per row.  S is
+//     read from tensor memory, P (bf16) written back over it as the A operand of P V.
+//     While one tile's softmax runs, the other tile's products do.
+//   - warps 8-11: bring K and V tiles (128 keys; 64 at head dim 256) into a ring in
+//     shared memory, 128-byte swizzled; fp8 values are widened to bf16 (exact).
+//   - warp 12: one thread issues every product.
+// Head dim 256 fits one query tile (its O takes half of tensor memory); its S is
+// double-buffered instead.
+//
+// The maximum m a row subtracts is only raised when its scores pass it by more than
+// 2^8 (weights up to 256 lose nothing in bf16 or fp32), so O is rescaled rarely.
+// Statistics and O are fp32; P's rounding to bf16 is the operands' common type.
+//
+// Keys a row must not see get weight exactly 0, but 0 * NaN is NaN in the product:
+// rows of V outside the cache row are zero-filled, and in the tiles that some row sees
+// only in part, NaN and infinite values of V are taken out and noted per dim; the
+// epilogue gives them back to the rows that see them.
+//
+// When the blocks are fewer than the SMs, each row is split over its keys, and
+// prefill_join merges the parts.  Every wait is bounded.
 #include <algorithm>
 
 #include <cuda_bf16.h>
 
 #include "keys.cuh"
+#include "stage.cuh"
 
 namespace tri {
 namespace {
 
-template <int D, int ELEM>
-__global__ void __launch_bounds__(128) prefill_kernel(const PrefillParams p) {
-    constexpr int E = D / 32;
+constexpr int kThreads = 512;
+constexpr int kRows = 128;  // rows of a query tile: one per thread of a softmax warpgroup
+constexpr float kRaise = 8.f;  // log2 of the most a weight may pass 1 before the maximum is raised
+
+template <int D>
+struct Cfg {
+    static constexpr int NT = D == 256 ? 1 : 2;     // query tiles per block
+    static constexpr int BN = D == 256 ? 64 : 128;  // keys per tile
+    static constexpr int kStageBytes = BN * D * 2;
+    static constexpr int kStages = D == 64 ? 8 : D == 128 ? 5 : 4;
+    static constexpr int kQBytes = kRows * D * 2;  // per query tile
+    static constexpr int kSubQ = kRows * 128;      // a 64-dim column of a Q tile
+    static constexpr int kSubK = BN * 128;         // ... of a K or V tile
+    // tensor memory columns
+    static constexpr int kTmemS(int b) { return b * BN; }  // S (and P) of tile b, or buffer b
+    static constexpr int kTmemO(int t) { return 256 + t * D; }
+    // shared memory from a 1024-byte aligned base
+    static constexpr int kSmRing = NT * kQBytes;
+    static constexpr int kSmBad = kSmRing + kStages * kStageBytes;  // int [3][D]
+    static constexpr int kSmBar = kSmBad + 3 * D * 4;
+    static constexpr int kBars = 2 * kStages + 1 + 2 + 2 + 2 + 1;
+    static constexpr int kSmMisc = kSmBar + kBars * 8;
+    static constexpr size_t kSmem = kSmMisc + 64 + 1024;
+};
+
+struct Misc {
+    uint32_t tmem;
+    volatile uint32_t abort_flag;
+    volatile uint32_t any_bad;      // a NaN or infinite value of V was taken out
+    volatile uint32_t any_missing;  // a slot without a block
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    // start, leading and stride byte offsets in 16-byte units, version 1, 128-byte swizzle
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16 instruction descriptor: fp32 accumulator, bf16 A and B, B K-major or MN-major.
+constexpr uint32_t idesc(int M, int N, int b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+        : "memory");
+}
+// A from tensor memory (bf16 pairs per 32-bit column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// -------------------------------------------------------------------- waits
+
+// Bounded wait of one role.  When it runs out the block is told to stop.
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Misc *misc, unsigned *flags) {
+    for (uint32_t it = 0; it < 64; it++)
+        if (mbar_test(bar, parity)) return true;
+    if (!misc->abort_flag && mbar_wait(bar, parity)) return true;
+    misc->abort_flag = 1u;
+    atomicOr(flags, TRI_FLAG_STAGE_TIMEOUT);
+    return false;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+template <int R>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// ---------------------------------------------------------------- arithmetic
+
+// Maxima that keep a NaN: a NaN score makes its row NaN, as the definition does.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max2(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ------------------------------------------------------------------ the work
+
+struct Block {
+    int l, h, seq;
+    int n;         // new tokens of the sequence
+    int rows;      // n * G
+    int row0;      // first row of this block
+    int len;       // N: slots of the cache row
+    int64_t tok0;  // tok_off[seq]
+    int64_t lo;    // row_off
+    int beg;       // first key tile (of the split)
+    int cnt[2];    // key tiles of each query tile, from beg
+    bool split_empty;
+};
+
+// Last slot row x (of the sequence's rows) sees.
+__device__ __forceinline__ int last_seen(const Block &b, int x, int G) { return b.len - b.n + x / G; }
+
+// The block's share of the work, by one warp: sequence after sequence, each cut into
+// ceil(n G / (128 NT)) blocks, the last rows (most keys) first.
+template <int D>
+__device__ __forceinline__ bool find_block(const PrefillParams &p, int64_t idx, int split, Block *out) {
+    constexpr int R = kRows * Cfg<D>::NT, BN = Cfg<D>::BN;
     const Geometry &geo = p.geo;
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t rows = p.T * geo.L * geo.Hq;
-    if (item >= rows) return;
-    const int g = (int)(item % geo.Hq);
-    const int64_t lt = item / geo.Hq, t = lt % p.T;
-    const int l = (int)(lt / p.T);
-    int s = 0;
-    for (; s < geo.S && p.tok_off[s + 1] <= t; s++)
-        if (p.tok_off[s + 1] < p.tok_off[s] && lane == 0) atomicOr(p.flags, TRI_FLAG_ROW_OFFSETS);
-    if (s == geo.S) return;
-    const int64_t tb = p.tok_off[s], te = p.tok_off[s + 1];
-    const int64_t r = ((int64_t)l * geo.S + s) * geo.H + g / geo.G;
-    const int64_t lo = geo.row_off[r], hi = geo.row_off[r + 1];
-    int64_t seen = hi - lo - (te - t) + 1;
-    if (lo < 0 || hi < lo || hi > geo.total || tb < 0 || tb > t || te > p.T) {
-        if (lane == 0) atomicOr(p.flags, TRI_FLAG_ROW_OFFSETS);
-        seen = 0;
-    }
-    float q[E], o[E] = {0.f}, m = -INFINITY, sum = 0.f;
-    for (int e = 0; e < E; e++) q[e] = __uint_as_float((uint32_t)p.q[item * D + lane * E + e] << 16) * p.scale_log2;
-    for (int64_t j = 0; j < seen; j++) {
-        int64_t rec = lo + j;
-        if (geo.layout == TRI_KV_PAGED) {
-            const int64_t bi = j >> geo.block_shift;
-            const int32_t blk = bi < geo.max_blocks ? __ldg(geo.block_table + (int64_t)s * geo.max_blocks + bi) : -1;
-            if (blk < 0 || blk >= geo.n_blocks) {
-                if (lane == 0) atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
-                continue;
-            }
-            rec = ((((int64_t)l * geo.n_blocks + blk) << geo.block_shift) | (j & ((1 << geo.block_shift) - 1))) * geo.H +
-                  g / geo.G;
-        }
-        float k[E], v[E];
-        for (int e = 0; e < E; e++) {
-            const int64_t x = rec * D + lane * E + e;
-            if (ELEM == 2) {
-                k[e] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p.K)[x] << 16);
-                v[e] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p.V)[x] << 16);
-            } else {
-                k[e] = e4m3x2_to_float2((uint8_t)p.K[x]).x;
-                v[e] = e4m3x2_to_float2((uint8_t)p.V[x]).x;
+    const int64_t lh = idx / p.blocks;
+    int64_t b = idx % p.blocks;
+    for (int base = 0; base < geo.S; base += 32) {
+        const int s = base + lane;
+        int64_t t0 = 0, n = 0;
+        if (s < geo.S) {
+            t0 = p.tok_off[s];
+            n = p.tok_off[s + 1] - t0;
+            if (t0 < 0 || n < 0 || t0 + n > p.T || (s == 0 && t0 != 0)) {
+                atomicOr(p.flags, TRI_FLAG_ROW_OFFSETS);
+                n = 0;
             }
         }
-        float dot = 0.f;
-        for (int e = 0; e < E; e++) dot = fmaf(q[e], k[e], dot);
-        for (int b = 16; b; b >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, b);
-        const float mn = fmaxf(m, dot);
-        const float a = m == mn ? 1.f : exp2f(m - mn), w = dot == -INFINITY ? 0.f : exp2f(dot - mn);
-        sum = fmaf(sum, a, w);
-        for (int e = 0; e < E; e++) o[e] = fmaf(o[e], a, w * v[e]);
-        m = mn;
+        const int64_t mine = (n * geo.G + R - 1) / R;
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, b < upto);
+        if (here) {
+            if (lane == __ffs(here) - 1) {
+                Block w;
+                w.l = (int)(lh / geo.H);
+                w.h = (int)(lh % geo.H);
+                w.seq = s;
+                w.n = (int)n;
+                w.rows = (int)(n * geo.G);
+                w.row0 = (int)(upto - 1 - b) * R;
+                w.tok0 = t0;
+                const int64_t r = ((int64_t)w.l * geo.S + s) * geo.H + w.h;
+                int64_t lo = geo.row_off[r], hi = geo.row_off[r + 1];
+                if (lo < 0 || hi < lo || hi > geo.total || hi - lo > 0x7fffff00LL) {
+                    atomicOr(p.flags, TRI_FLAG_ROW_OFFSETS);
+                    hi = lo = 0;
+                }
+                w.lo = lo;
+                w.len = (int)(hi - lo);
+                int c[2] = {0, 0};
+                for (int t = 0; t < Cfg<D>::NT; t++) {
+                    const int first = w.row0 + t * kRows;
+                    if (first < w.rows) c[t] = max(0, last_seen(w, min(first + kRows, w.rows) - 1, geo.G) + BN) / BN;
+                }
+                const int all = max(c[0], c[1]);
+                w.beg = (int)((int64_t)all * split / p.splits);
+                const int end = (int)((int64_t)all * (split + 1) / p.splits);
+                for (int t = 0; t < 2; t++) w.cnt[t] = max(0, min(c[t], end) - w.beg);
+                *out = w;
+            }
+            if (idx == 0)  // the first block looks at the offsets of the sequences behind its own, too
+                for (int x = s + 32; x < geo.S; x += 32)
+                    if (p.tok_off[x] > p.tok_off[x + 1] || p.tok_off[x + 1] > p.T) atomicOr(p.flags, TRI_FLAG_ROW_OFFSETS);
+            return true;
+        }
+        b -= __shfl_sync(0xffffffffu, upto, 31);
     }
-    for (int e = 0; e < E; e++) {
-        const __nv_bfloat16 b = __float2bfloat16_rn(sum == 0.f ? 0.f : o[e] / sum);
-        p.out[item * D + lane * E + e] = *reinterpret_cast<const uint16_t *>(&b);
+    return false;
+}
+
+// Record of slot j of the block's row; -1 if its table names none.
+__device__ __forceinline__ int64_t record(const Geometry &geo, const Block &b, int j) {
+    if (geo.layout != TRI_KV_PAGED) return b.lo + j;
+    const int bi = j >> geo.block_shift;
+    const int32_t blk = bi < geo.max_blocks ? __ldg(geo.block_table + (int64_t)b.seq * geo.max_blocks + bi) : -1;
+    if (blk < 0 || blk >= geo.n_blocks) return -1;
+    return ((((int64_t)b.l * geo.n_blocks + blk) << geo.block_shift) | (j & ((1 << geo.block_shift) - 1))) * geo.H + b.h;
+}
+
+// Byte of (row, 16-byte chunk c of d) in a swizzled tile whose 64-dim columns are `sub` bytes.
+__device__ __forceinline__ uint32_t tile_at(int row, int c, int sub) {
+    return (uint32_t)((c >> 3) * sub + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+
+// ------------------------------------------------------------------- loading
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// Takes NaN and infinities out of 8 bf16 values of V (dims d0.., slot j), noting for
+// each dim the first slot that has one: bad[0] NaN, bad[1] +inf, bad[2] -inf.
+template <int D>
+__device__ __forceinline__ uint4 take_out(uint4 v, int d0, int j, int *bad, Misc *misc) {
+    misc->any_bad = 1u;
+    const auto word = [&](uint32_t w, int d) {
+#pragma unroll 1
+        for (int k = 0; k < 2; k++) {
+            const uint32_t x = (w >> (16 * k)) & 0xffffu;
+            if ((x & 0x7f80u) != 0x7f80u) continue;
+            const int kind = (x & 0x7fu) ? 0 : (x & 0x8000u) ? 2 : 1;
+            atomicMin(bad + kind * D + d + k, j);
+            w &= ~(0xffffu << (16 * k));
+        }
+        return w;
+    };
+    return make_uint4(word(v.x, d0), word(v.y, d0 + 2), word(v.z, d0 + 4), word(v.w, d0 + 6));
+}
+__device__ __forceinline__ bool has_special(uint4 v) {
+    const auto one = [&](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+    return one(v.x) || one(v.y) || one(v.z) || one(v.w);
+}
+
+// Eight e4m3 values (two words) as bf16.
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
+    const float2 x = e4m3x2_to_float2(a), y = e4m3x2_to_float2(a >> 16), z = e4m3x2_to_float2(b), w = e4m3x2_to_float2(b >> 16);
+    return make_uint4(bf16x2(x.x, x.y), bf16x2(y.x, y.y), bf16x2(z.x, z.y), bf16x2(w.x, w.y));
+}
+
+// The loader warps: fill 2j is K, fill 2j+1 V of key tile beg + j.  bf16 rows are copied
+// asynchronously, kLag fills in flight before the oldest is handed over.
+template <int D, int ELEM>
+__device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, unsigned char *sm, uint64_t *full,
+                                       uint64_t *empty, int *bad, Misc *misc) {
+    using C = Cfg<D>;
+    constexpr int BN = C::BN, CH = D * ELEM / 16, PER = BN * CH / 128;  // 16-byte chunks per record, per thread
+    constexpr int kLag = 2;
+    const Geometry &geo = p.geo;
+    const int tid = threadIdx.x & 127;
+    const int tiles = max(b.cnt[0], b.cnt[1]);
+    const uint32_t ring = smem_u32(sm + C::kSmRing);
+    // Tiles from the first that some row of query tile t sees only in part.
+    int first[2];
+    for (int t = 0; t < 2; t++) first[t] = last_seen(b, b.row0 + t * kRows, geo.G) + 1;
+    const auto partial = [&](int j) {
+        const int end = (b.beg + j + 1) * BN;
+        return (j < b.cnt[0] && end > first[0]) || (j < b.cnt[1] && end > first[1]);
+    };
+    // Hands fill f over: its V may need special values taken out first.
+    const auto hand_over = [&](int f) {
+        const int j = f >> 1;
+        if (ELEM == 2 && (f & 1) && partial(j)) {
+            unsigned char *st = sm + C::kSmRing + (f % C::kStages) * C::kStageBytes;
+            for (int k = 0; k < PER; k++) {
+                const int e = tid + 128 * k, row = e / CH, c = e % CH;
+                uint4 *at = reinterpret_cast<uint4 *>(st + tile_at(row, c, C::kSubK));
+                const uint4 v = *at;
+                if (has_special(v)) *at = take_out<D>(v, 8 * c, (b.beg + j) * BN + row, bad, misc);
+            }
+        }
+        fence_async_smem();
+        mbar_arrive(full + f % C::kStages);
+    };
+    for (int f = 0; f < 2 * tiles; f++) {
+        const int st = f % C::kStages;
+        if (f >= C::kStages && !role_wait(empty + st, ((f / C::kStages) - 1) & 1, misc, p.flags)) break;
+        const char *src = f & 1 ? p.V : p.K;
+        const int key0 = (b.beg + (f >> 1)) * BN;
+        if (ELEM == 2) {
+#pragma unroll 4
+            for (int k = 0; k < PER; k++) {
+                const int e = tid + 128 * k, row = e / CH, c = e % CH, j = key0 + row;
+                int64_t rec = j < b.len ? record(geo, b, j) : -1;
+                if (rec < 0 && j < b.len) {
+                    misc->any_missing = 1u;
+                    atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
+                }
+                cp16(ring + st * C::kStageBytes + tile_at(row, c, C::kSubK), src + (rec < 0 ? 0 : rec) * (2 * D) + 16 * c,
+                     rec >= 0);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (f >= kLag) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+                hand_over(f - kLag);
+            }
+        } else {
+            uint4 v[PER];
+#pragma unroll
+            for (int k = 0; k < PER; k++) {
+                const int e = tid + 128 * k, row = e / CH, c = e % CH, j = key0 + row;
+                const int64_t rec = j < b.len ? record(geo, b, j) : -1;
+                if (rec < 0 && j < b.len) {
+                    misc->any_missing = 1u;
+                    atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
+                }
+                v[k] = rec < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(src + rec * D + 16 * c);
+            }
+            const bool chk = (f & 1) && partial(f >> 1);
+#pragma unroll
+            for (int k = 0; k < PER; k++) {
+                const int e = tid + 128 * k, row = e / CH, c = e % CH;
+                uint4 lo = widen8(v[k].x, v[k].y), hi = widen8(v[k].z, v[k].w);
+                if (chk && has_special(lo)) lo = take_out<D>(lo, 16 * c, key0 + row, bad, misc);
+                if (chk && has_special(hi)) hi = take_out<D>(hi, 16 * c + 8, key0 + row, bad, misc);
+                unsigned char *at = sm + C::kSmRing + st * C::kStageBytes;
+                *reinterpret_cast<uint4 *>(at + tile_at(row, 2 * c, C::kSubK)) = lo;
+                *reinterpret_cast<uint4 *>(at + tile_at(row, 2 * c + 1, C::kSubK)) = hi;
+            }
+            hand_over(f);
+        }
     }
-    if (p.lse && lane == 0) p.lse[item] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+    if (ELEM == 2) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (!misc->abort_flag)
+            for (int f = max(0, 2 * tiles - kLag); f < 2 * tiles; f++) hand_over(f);
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t q, uint32_t k, uint32_t d) {
+    using C = Cfg<D>;
+#pragma unroll
+    for (int i = 0; i < D / 16; i++)
+        mma_ss(d, smem_desc(q + (i >> 2) * C::kSubQ + (i & 3) * 32, 16, 1024),
+               smem_desc(k + (i >> 2) * C::kSubK + (i & 3) * 32, 16, 1024), idesc(kRows, C::BN, 0), i > 0);
+}
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t p, uint32_t v, uint32_t d, bool acc) {
+    using C = Cfg<D>;
+#pragma unroll
+    for (int i = 0; i < C::BN / 16; i++)
+        mma_ts(d, p + 8 * i, smem_desc(v + i * 2048, C::kSubK, 1024), idesc(kRows, D, 1), acc || i > 0);
 }
 
 template <int D>
-cudaError_t launch_d(const PrefillParams &p, cudaStream_t s) {
-    const int64_t blocks = (p.T * p.geo.L * p.geo.Hq + 3) / 4;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (p.geo.elem_bytes == 2) prefill_kernel<D, 2><<<(unsigned)blocks, 128, 0, s>>>(p);
-    else prefill_kernel<D, 1><<<(unsigned)blocks, 128, 0, s>>>(p);
-    return cudaGetLastError();
+__device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, unsigned char *sm, uint32_t tmem,
+                                       uint64_t *full, uint64_t *empty, uint64_t *q_full, uint64_t *s_full,
+                                       uint64_t *p_full, uint64_t *o_done, Misc *misc) {
+    using C = Cfg<D>;
+    const int tiles = max(b.cnt[0], b.cnt[1]);
+    const uint32_t q = smem_u32(sm), ring = smem_u32(sm + C::kSmRing);
+    const auto have = [&](int f) {
+        const bool ok = role_wait(full + f % C::kStages, (f / C::kStages) & 1, misc, p.flags);
+        fence_after();
+        return ok;
+    };
+    const auto at = [&](int f) { return ring + (f % C::kStages) * C::kStageBytes; };
+    if (tiles == 0 || !role_wait(q_full, 0, misc, p.flags)) return;
+    if (!have(0)) return;
+    if (C::NT == 2) {
+        for (int t = 0; t < 2; t++)
+            if (b.cnt[t] > 0) {
+                issue_qk<D>(q + t * C::kQBytes, at(0), tmem + C::kTmemS(t));
+                mma_commit(s_full + t);
+            }
+        mma_commit(empty);
+        for (int j = 0; j < tiles; j++) {
+            bool v = false, k = false;  // V of tile j, K of tile j + 1 have landed
+            for (int t = 0; t < 2; t++) {
+                if (j >= b.cnt[t]) continue;
+                if (!role_wait(p_full + t, j & 1, misc, p.flags)) return;
+                if (!v && !have(2 * j + 1)) return;
+                v = true;
+                fence_after();
+                issue_pv<D>(tmem + C::kTmemS(t), at(2 * j + 1), tmem + C::kTmemO(t), j > 0);
+                if (j + 1 == b.cnt[t]) mma_commit(o_done + t);
+                // the last query tile that takes V
+                if (t == 1 || j >= b.cnt[1]) mma_commit(empty + (2 * j + 1) % C::kStages);
+                if (j + 1 < b.cnt[t]) {
+                    if (!k && !have(2 * j + 2)) return;
+                    k = true;
+                    issue_qk<D>(q + t * C::kQBytes, at(2 * j + 2), tmem + C::kTmemS(t));
+                    mma_commit(s_full + t);
+                    if (t == 1 || j + 1 >= b.cnt[1]) mma_commit(empty + (2 * j + 2) % C::kStages);
+                }
+            }
+        }
+    } else {
+        issue_qk<D>(q, at(0), tmem + C::kTmemS(0));
+        mma_commit(s_full);
+        mma_commit(empty);
+        for (int j = 0; j < tiles; j++) {
+            if (j + 1 < tiles) {
+                if (!have(2 * j + 2)) return;
+                issue_qk<D>(q, at(2 * j + 2), tmem + C::kTmemS((j + 1) & 1));
+                mma_commit(s_full + ((j + 1) & 1));
+                mma_commit(empty + (2 * j + 2) % C::kStages);
+            }
+            if (!role_wait(p_full + (j & 1), (j >> 1) & 1, misc, p.flags) || !have(2 * j + 1)) return;
+            issue_pv<D>(tmem + C::kTmemS(j & 1), at(2 * j + 1), tmem + C::kTmemO(0), j > 0);
+            mma_commit(empty + (2 * j + 1) % C::kStages);
+            mma_commit(o_done);  // phase j
+        }
+    }
+}
+
+// ------------------------------------------------------------------- softmax
+
+template <int D>
+__device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, int t, int64_t part, unsigned char *sm,
+                                        uint32_t tmem, uint64_t *q_full, uint64_t *s_full, uint64_t *p_full,
+                                        uint64_t *o_done, const int *bad, Misc *misc) {
+    using C = Cfg<D>;
+    constexpr int BN = C::BN;
+    const Geometry &geo = p.geo;
+    const int tid = threadIdx.x & 127, lane = tid & 31;
+    const int G = geo.G;
+    const int base = b.row0 + t * kRows;  // first row of the tile
+    // The query tile: 16-byte chunks, rows behind the sequence's last as zeros.
+    for (int e = tid; e < kRows * D / 8; e += 128) {
+        const int row = e / (D / 8), c = e % (D / 8), x = base + row;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (x < b.rows)
+            v = *reinterpret_cast<const uint4 *>(
+                p.q + (((int64_t)b.l * p.T + b.tok0 + x / G) * geo.Hq + b.h * G + x % G) * D + 8 * c);
+        *reinterpret_cast<uint4 *>(sm + t * C::kQBytes + tile_at(row, c, C::kSubQ)) = v;
+    }
+    fence_async_smem();
+    mbar_arrive(q_full);
+
+    const int x = base + tid;
+    const bool real = x < b.rows;
+    // rows behind the last see what the last does; they are not written
+    const int limit = last_seen(b, min(x, b.rows - 1), G);
+    const int first = last_seen(b, base, G);  // no row of the tile sees less
+    const uint32_t my = tmem + ((uint32_t)(tid & ~31) << 16);
+    const float scale = p.scale_log2;
+    float m = -INFINITY, sum = 0.f;  // m in units of log2: subtracted from scaled scores
+    bool ok = true;
+    for (int j = 0; j < b.cnt[t]; j++) {
+        const int sb = C::NT == 2 ? t : j & 1;
+        const uint32_t ph = C::NT == 2 ? j & 1 : (j >> 1) & 1;
+        if (!role_wait(s_full + sb, ph, misc, p.flags)) { ok = false; break; }
+        fence_after();
+        uint32_t s[BN];
+#pragma unroll
+        for (int c = 0; c < BN / 32; c++) tmem_ld32(my + C::kTmemS(sb) + 32 * c, s + 32 * c);
+        wait_ld();
+        const int key0 = (b.beg + j) * BN;
+        if (key0 + BN - 1 > first) {  // some row sees the tile only in part
+#pragma unroll
+            for (int k = 0; k < BN; k++)
+                if (key0 + k > limit) s[k] = 0xff800000u;
+        }
+        if (misc->any_missing) {  // slots without a block have no weight
+            for (int c = 0; c < BN / 32; c++) {
+                const int jj = key0 + 32 * c + lane;
+                const uint32_t gone = __ballot_sync(0xffffffffu, jj < b.len && record(geo, b, jj) < 0);
+#pragma unroll
+                for (int k = 0; k < BN; k++)
+                    if ((k >> 5) == c && (gone >> (k & 31) & 1)) s[k] = 0xff800000u;
+            }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            constexpr int W = BN / 4;
+            mx[c] = max2(__uint_as_float(s[c * W]), __uint_as_float(s[c * W + 1]));
+#pragma unroll
+            for (int k = 2; k < W; k += 2) mx[c] = max3(mx[c], __uint_as_float(s[c * W + k]), __uint_as_float(s[c * W + k + 1]));
+        }
+        float top = max2(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+        if (top == INFINITY) top = NAN;  // inf - inf, as the definition has it
+        // raise the maximum: always from nothing, else once the scores pass it by 2^8
+        if (__any_sync(0xffffffffu, !(top <= m + kRaise))) {
+            const float mn = top <= m + kRaise ? m : top;
+            const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+            if (j > 0) {
+                if (C::NT == 1 && !role_wait(o_done, (j - 1) & 1, misc, p.flags)) { ok = false; break; }
+                fence_after();
+                const float f1 = mn == m ? 1.f : f;
+#pragma unroll
+                for (int c = 0; c < D / 32; c++) {
+                    uint32_t o[32];
+                    tmem_ld32(my + C::kTmemO(t) + 32 * c, o);
+                    wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f1);
+                    tmem_st32(my + C::kTmemO(t) + 32 * c, o);
+                }
+                sum *= f1;
+            }
+            m = mn;
+        }
+        const float off = m == -INFINITY ? 0.f : -m;
+        float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < BN / 32; c++) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+                const float a = ex2(fmaf(__uint_as_float(s[32 * c + 2 * k]), scale, off));
+                const float d = ex2(fmaf(__uint_as_float(s[32 * c + 2 * k + 1]), scale, off));
+                part_sum[(2 * k) & 3] += a;
+                part_sum[(2 * k + 1) & 3] += d;
+                pk[k] = bf16x2(a, d);
+            }
+            tmem_st16(my + C::kTmemS(sb) + 16 * c, pk);
+        }
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + sb);
+        sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+    }
+    // ---- epilogue
+    if (ok && b.cnt[t] > 0) {
+        ok = role_wait(o_done + (C::NT == 2 ? t : 0), C::NT == 2 ? 0 : (b.cnt[t] - 1) & 1, misc, p.flags);
+        fence_after();
+    }
+    if (!ok) return;
+    const bool nothing = sum == 0.f;
+    const float inv = nothing ? 0.f : 1.f / sum;
+    const int64_t row = ((int64_t)b.l * p.T + b.tok0 + x / G) * geo.Hq + b.h * G + x % G;
+    if (part < 0 && real && p.lse) p.lse[row] = nothing ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+    float *slab = p.part + part * (C::NT * kRows) * (D + 2) + (t * kRows + tid) * (D + 2);
+    if (part >= 0) {
+        slab[D] = nothing ? -INFINITY : m;
+        slab[D + 1] = sum;
+    }
+    const bool fix = misc->any_bad;
+#pragma unroll
+    for (int c = 0; c < D / 32; c++) {
+        uint32_t o[32];
+        if (b.cnt[t] > 0) {
+            tmem_ld32(my + C::kTmemO(t) + 32 * c, o);
+            wait_ld();
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; k++) o[k] = 0u;
+        }
+        if (fix && b.cnt[t] > 0) {
+#pragma unroll
+            for (int k = 0; k < 32; k++) {
+                const int *at = bad + 32 * c + k;
+                if (at[D] <= limit) o[k] = __float_as_uint(__uint_as_float(o[k]) + INFINITY);
+                if (at[2 * D] <= limit) o[k] = __float_as_uint(__uint_as_float(o[k]) - INFINITY);
+                if (at[0] <= limit) o[k] = 0x7fc00000u;
+            }
+        }
+        if (part >= 0) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 2)
+                *reinterpret_cast<uint2 *>(slab + 32 * c + k) = make_uint2(o[k], o[k + 1]);
+        } else if (real) {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * D + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const auto two = [&](int i) {
+                    return bf16x2(__uint_as_float(o[8 * k + i]) * inv, __uint_as_float(o[8 * k + i + 1]) * inv);
+                };
+                dst[k] = make_uint4(two(0), two(2), two(4), two(6));
+            }
+        }
+    }
+    fence_before();
+}
+
+// ------------------------------------------------------------------- kernels
+
+template <int D, int ELEM>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
+    using C = Cfg<D>;
+    extern __shared__ unsigned char smraw[];
+    __shared__ Block blk;
+    __shared__ int found;
+    unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    int *bad = reinterpret_cast<int *>(sm + C::kSmBad);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kSmBar), *empty = full + C::kStages;
+    uint64_t *q_full = empty + C::kStages, *s_full = q_full + 1, *p_full = s_full + 2, *o_done = p_full + 2,
+             *drain = o_done + 2;
+    Misc *misc = reinterpret_cast<Misc *>(sm + C::kSmMisc);
+    const int warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    const int split = (int)(blockIdx.x % p.splits);
+    const int64_t idx = blockIdx.x / p.splits;
+    if (warp == 0) {
+        const bool f = find_block<D>(p, idx, split, &blk);
+        if ((threadIdx.x & 31) == 0) found = f;
+    }
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < C::kStages; i++) {
+            mbar_init(full + i, 128);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(q_full, 128 * C::NT);
+        mbar_init(drain, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(o_done + i, 1);
+        }
+        mbar_init_fence();
+        misc->abort_flag = 0u;
+        misc->any_bad = 0u;
+        misc->any_missing = 0u;
+    }
+    for (int e = threadIdx.x; e < 3 * D; e += kThreads) bad[e] = 0x7fffffff;
+    __syncthreads();
+    if (!found) return;
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&misc->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = misc->tmem;
+    // Registers: 512 threads are launched with 128 each; 2 x 200 + 72 + 40 = 4 x 128.
+    if (warp < 8) {
+        regs_up<200>();
+        const int t = warp >> 2;
+        if (t < C::NT)
+            softmax<D>(p, blk, t, p.splits > 1 ? (int64_t)blockIdx.x : -1, sm, tmem, q_full, s_full, p_full, o_done, bad, misc);
+    } else if (warp < 12) {
+        regs_down<72>();
+        loader<D, ELEM>(p, blk, sm, full, empty, bad, misc);
+    } else {
+        regs_down<40>();
+        if (threadIdx.x == 12 * 32) {
+            issuer<D>(p, blk, sm, tmem, full, empty, q_full, s_full, p_full, o_done, misc);
+            if (misc->abort_flag) {  // after a wait ran out: products in flight end before their memory is released
+                mma_commit(drain);
+                mbar_wait(drain, 0);
+            }
+        }
+        __syncwarp();
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    grid_dependents_launch();
+}
+
+// Merges the splits of a block's rows: one warp per row,
+//   out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ PrefillParams p) {
+    constexpr int R = kRows * Cfg<D>::NT, PER = R / 8;  // blocks of 8 rows per unit
+    __shared__ Block blk;
+    __shared__ int found;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Geometry &geo = p.geo;
+    grid_dependency_wait();
+    const int64_t idx = blockIdx.x / PER;
+    const int r = (int)(blockIdx.x % PER) * 8 + warp;
+    if (warp == 0) {
+        const bool f = find_block<D>(p, idx, 0, &blk);
+        if (lane == 0) found = f;
+    }
+    __syncthreads();
+    const int x = blk.row0 + r;
+    if (!found || x >= blk.rows) return;
+    const float *slab = p.part + idx * p.splits * (int64_t)R * (D + 2) + (int64_t)r * (D + 2);
+    float m = -INFINITY;
+    for (int k = 0; k < p.splits; k++) m = max2(m, slab[(int64_t)k * R * (D + 2) + D]);
+    float sum = 0.f, o[D / 32] = {0.f};
+    for (int k = 0; k < p.splits; k++) {
+        const float *s = slab + (int64_t)k * R * (D + 2);
+        const float mk = s[D];
+        if (mk == -INFINITY) continue;
+        const float w = exp2f(mk - m);
+        sum = fmaf(w, s[D + 1], sum);
+#pragma unroll
+        for (int e = 0; e < D / 32; e++) o[e] = fmaf(w, s[lane + 32 * e], o[e]);
+    }
+    const int64_t row = ((int64_t)blk.l * p.T + blk.tok0 + x / geo.G) * geo.Hq + blk.h * geo.G + x % geo.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < D / 32; e++) {
+        const __nv_bfloat16 v = __float2bfloat16_rn(o[e] * inv);
+        p.out[row * D + lane + 32 * e] = *reinterpret_cast<const uint16_t *>(&v);
+    }
+    if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Blocks per (layer, KV head): sum over sequences of ceil(n G / R), bounded from what the host knows.
+int64_t most_blocks(int64_t S, int64_t G, int D, int64_t T) {
+    const int64_t R = D == 256 ? kRows : 2 * kRows;
+    return T * G / R + std::min(S, T);
+}
+
+constexpr int kMostParts = 160;  // parts of split rows the workspace holds: one per SM
+
+// Splits of each row over its keys: as many as fill the SMs while a split keeps at least
+// four key tiles of the average row.
+int splits_of(int64_t blocks, int64_t keys, int D) {
+    const int64_t tiles = keys / (D == 256 ? 64 : 128);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sm_count(), kMostParts) / std::max<int64_t>(1, blocks), tiles / 4));
+}
+
+template <int D, int ELEM>
+cudaError_t launch_t(const PrefillParams &p, int64_t units, cudaStream_t s) {
+    static bool attr[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr[dev & 63]) {
+        cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, ELEM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        attr[dev & 63] = true;
+    }
+    cudaError_t e = launch_pdl(prefill_kernel<D, ELEM>, dim3((unsigned)(units * p.splits)), dim3(kThreads), Cfg<D>::kSmem, s, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_pdl(prefill_join<D>, dim3((unsigned)(units * Cfg<D>::NT * kRows / 8)), dim3(256), 0, s, p);
+}
+
+template <int D>
+cudaError_t launch_d(const PrefillParams &p0, cudaStream_t s) {
+    PrefillParams p = p0;
+    const Geometry &geo = p.geo;
+    p.blocks = most_blocks(geo.S, geo.G, D, p.T);
+    const int64_t units = p.blocks * geo.L * geo.H;
+    if (units > 0x7fffffffLL / 64 || p.T * geo.G > 0x7fffff00LL) return cudaErrorInvalidConfiguration;
+    p.splits = splits_of(units, geo.total / ((int64_t)geo.L * geo.S * geo.H), D);
+    return geo.elem_bytes == 2 ? launch_t<D, 2>(p, units, s) : launch_t<D, 1>(p, units, s);
 }
 
 }  // namespace
 
-size_t prefill_scratch_bytes(int64_t, int64_t, int64_t, int64_t, int, int64_t) { return 0; }
+// Scratch of split rows: at most one part per SM.
+size_t prefill_scratch_bytes(int64_t L, int64_t S, int64_t H, int64_t G, int D, int64_t T) {
+    const int64_t units = most_blocks(S, G, D, T) * L * H, sms = kMostParts;
+    if (units == 0 || units > sms / 2) return 0;
+    return (size_t)(sms / units * units) * (D == 256 ? kRows : 2 * kRows) * (D + 2) * sizeof(float);
+}
 
 cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s) {
     switch (p.geo.D) {

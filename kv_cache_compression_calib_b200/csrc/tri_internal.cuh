@@ -167,6 +167,8 @@ struct PrefillParams {
     float *lse;         // [L][T][Hq] or null
     float *part;        // scratch of split rows
     unsigned *flags;
+    int64_t blocks;  // bound of the blocks per (layer, KV head), set at launch
+    int32_t splits;  // parts each row's keys are cut into, set at launch
 };
 
 constexpr int kFusedMaxRow = TRI_FUSED_MAX_ROW;  // longest row the fused score-and-select kernel holds on chip
