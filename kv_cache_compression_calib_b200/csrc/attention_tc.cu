@@ -31,10 +31,8 @@
 // (TRI_FLAG_STAGE_TIMEOUT); tensor memory is released before the CTA exits.
 #include <algorithm>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "stage.cuh"
+#include "tensormap.cuh"
 
 namespace tri {
 
@@ -465,23 +463,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 namespace {
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link to libcuda).
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
-    return fn;
-}
-
 // A [total][128] bf16 matrix as 64-dim x 128-key boxes, 128-byte swizzle.
 bool make_map(CUtensorMap *m, const void *base, int64_t total) {
-    auto fn = encode_fn();
+    auto fn = tensormap_encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)kTcD, (cuuint64_t)total};
     const cuuint64_t strides[1] = {(cuuint64_t)kTcD * 2};

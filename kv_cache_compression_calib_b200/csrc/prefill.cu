@@ -16,7 +16,11 @@
 //     read from tensor memory, P (bf16) written back over it as the A operand of P V.
 //     While one tile's softmax runs, the other tile's products do.
 //   - warps 8-11: bring K and V tiles (128 keys; 64 at head dim 256) into a ring in
-//     shared memory, 128-byte swizzled; fp8 values are widened to bf16 (exact).
+//     shared memory, 128-byte swizzled.  bf16 caches: warp 8 issues TMA copies, one
+//     box per 64 dims of a contiguous tile or of a block of pages, and warps 9-11
+//     only touch V tiles that some row sees in part.  fp8 caches, and blocks too
+//     small for a swizzle atom (8 slots): all four warps copy, fp8 widened to bf16
+//     (exact).
 //   - warp 12: one thread issues every product.
 // Head dim 256 fits one query tile (its O takes half of tensor memory); its S is
 // double-buffered instead.
@@ -38,6 +42,7 @@
 
 #include "keys.cuh"
 #include "stage.cuh"
+#include "tensormap.cuh"
 
 namespace tri {
 namespace {
@@ -62,7 +67,7 @@ struct Cfg {
     static constexpr int kSmRing = NT * kQBytes;
     static constexpr int kSmBad = kSmRing + kStages * kStageBytes;  // int [3][D]
     static constexpr int kSmBar = kSmBad + 3 * D * 4;
-    static constexpr int kBars = 2 * kStages + 1 + 2 + 2 + 2 + 1;
+    static constexpr int kBars = 3 * kStages + 1 + 2 + 2 + 2 + 1;
     static constexpr int kSmMisc = kSmBar + kBars * 8;
     static constexpr size_t kSmem = kSmMisc + 64 + 1024;
 };
@@ -321,7 +326,134 @@ __device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
     return make_uint4(bf16x2(x.x, x.y), bf16x2(y.x, y.y), bf16x2(z.x, z.y), bf16x2(w.x, w.y));
 }
 
-// The loader warps: fill 2j is K, fill 2j+1 V of key tile beg + j.  bf16 rows are copied
+// Query tile t's first row sees this many slots: key tiles past them are seen in part.
+struct Partial {
+    int beg, cnt[2], first[2];
+    __device__ __forceinline__ Partial(const Block &b, int G) {
+        beg = b.beg;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            cnt[t] = b.cnt[t];
+            first[t] = last_seen(b, b.row0 + t * kRows, G) + 1;
+        }
+    }
+    template <int BN>
+    __device__ __forceinline__ bool tile(int j) const {
+        const int end = (beg + j + 1) * BN;
+        return (j < cnt[0] && end > first[0]) || (j < cnt[1] && end > first[1]);
+    }
+};
+
+__device__ __forceinline__ void tma2(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The TMA warp of a bf16 cache.  Fill 2j is K, fill 2j+1 V of key tile beg + j.  A V
+// tile that is seen in part lands on land[stage], for the mending warps; every other
+// fill on full[stage].
+template <int D>
+__device__ __forceinline__ void tma_loader(const PrefillParams &p, const Block &b, unsigned char *sm, const CUtensorMap *mk,
+                                           const CUtensorMap *mv, uint64_t *full, uint64_t *empty, uint64_t *land,
+                                           Misc *misc) {
+    using C = Cfg<D>;
+    constexpr int BN = C::BN;
+    const Geometry &geo = p.geo;
+    const int lane = threadIdx.x & 31;
+    const int tiles = max(b.cnt[0], b.cnt[1]);
+    const uint32_t ring = smem_u32(sm + C::kSmRing);
+    const Partial part(b, geo.G);
+    const bool paged = geo.layout == TRI_KV_PAGED;
+    const int64_t lo = b.lo;
+    const int len = b.len, beg = b.beg, h = b.h;
+    const int32_t *table = geo.block_table + (int64_t)b.seq * geo.max_blocks;
+    const int box = paged ? min(1 << geo.block_shift, BN) : BN;  // slots per copy
+    const int64_t layer = (int64_t)b.l * geo.n_blocks;
+    for (int f = 0; f < 2 * tiles; f++) {
+        const int st = f % C::kStages;
+        const bool v = f & 1;
+        const int key0 = (beg + (f >> 1)) * BN;
+        // Slot of the pool the lane's copy starts at (looked up before the wait below).
+        int64_t slot = -1;
+        const int j = key0 + lane * box;
+        const bool mine = lane * box < BN && j < len;
+        if (paged && mine) {
+            const int bi = j >> geo.block_shift;
+            const int32_t blk = bi < geo.max_blocks ? __ldg(table + bi) : -1;
+            if (blk >= 0 && blk < geo.n_blocks)
+                slot = ((layer + blk) << geo.block_shift) + (j & ((1 << geo.block_shift) - 1));
+        } else if (mine) {
+            slot = lo + j;
+        }
+        if (f >= C::kStages && !role_wait(empty + st, ((f / C::kStages) - 1) & 1, misc, p.flags)) break;
+        uint64_t *bar = v && part.tile<BN>(f >> 1) ? land + st : full + st;
+        const uint32_t dst = ring + st * C::kStageBytes;
+        const uint32_t here = __ballot_sync(0xffffffffu, slot >= 0);
+        if (here != __ballot_sync(0xffffffffu, mine)) {  // blocks that the table does not name
+            misc->any_missing = 1u;
+            if (mine && slot < 0) {
+                atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
+                if (v)  // no weight reaches their keys; their values must be finite
+                    for (int x = 0; x < D / 64; x++)
+                        for (int e = 0; e < box * 8; e++)
+                            *reinterpret_cast<uint4 *>(sm + C::kSmRing + st * C::kStageBytes + x * C::kSubK +
+                                                       lane * box * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+            __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(here) * box * D * 2));
+        __syncwarp();
+        if (slot >= 0) {
+            const CUtensorMap *map = v ? mv : mk;
+#pragma unroll
+            for (int x = 0; x < D / 64; x++) {
+                const uint32_t at = dst + x * C::kSubK + lane * box * 128;
+                if (paged) tma3(at, map, 64 * x, h, (int)slot, bar);
+                else tma2(at, map, 64 * x, (int)slot, bar);
+            }
+        }
+    }
+}
+
+// Warps 9-11 beside the TMA warp: V tiles seen in part get zeros behind the row and
+// their special values taken out, then pass on to full[stage].
+template <int D>
+__device__ __forceinline__ void mender(const PrefillParams &p, const Block &b, unsigned char *sm, uint64_t *full,
+                                       uint64_t *land, int *bad, Misc *misc) {
+    using C = Cfg<D>;
+    constexpr int BN = C::BN, CH = D / 8;
+    const int tid = threadIdx.x - 9 * 32;
+    const int tiles = max(b.cnt[0], b.cnt[1]);
+    const Partial part(b, p.geo.G);
+    uint32_t phase = 0;  // bit st: parity of land[st]
+    for (int j = 0; j < tiles; j++) {
+        if (!part.tile<BN>(j)) continue;
+        const int st = (2 * j + 1) % C::kStages, key0 = (b.beg + j) * BN;
+        if (!role_wait(land + st, (phase >> st) & 1u, misc, p.flags)) break;
+        phase ^= 1u << st;
+        unsigned char *at = sm + C::kSmRing + st * C::kStageBytes;
+        for (int e = tid; e < BN * CH; e += 96) {
+            const int row = e / CH, c = e % CH;
+            uint4 *w = reinterpret_cast<uint4 *>(at + tile_at(row, c, C::kSubK));
+            if (key0 + row >= b.len) *w = make_uint4(0u, 0u, 0u, 0u);
+            else if (const uint4 x = *w; has_special(x)) *w = take_out<D>(x, 8 * c, key0 + row, bad, misc);
+        }
+        fence_async_smem();
+        asm volatile("bar.sync 1, 96;" ::: "memory");
+        if (tid == 0) mbar_arrive(full + st);
+    }
+}
+
+// All four warps, for what TMA does not bring: fill 2j is K, fill 2j+1 V of key tile beg + j.  bf16 rows are copied
 // asynchronously, kLag fills in flight before the oldest is handed over.
 template <int D, int ELEM>
 __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, unsigned char *sm, uint64_t *full,
@@ -333,17 +465,11 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
     const int tid = threadIdx.x & 127;
     const int tiles = max(b.cnt[0], b.cnt[1]);
     const uint32_t ring = smem_u32(sm + C::kSmRing);
-    // Tiles from the first that some row of query tile t sees only in part.
-    int first[2];
-    for (int t = 0; t < 2; t++) first[t] = last_seen(b, b.row0 + t * kRows, geo.G) + 1;
-    const auto partial = [&](int j) {
-        const int end = (b.beg + j + 1) * BN;
-        return (j < b.cnt[0] && end > first[0]) || (j < b.cnt[1] && end > first[1]);
-    };
+    const Partial part(b, geo.G);
     // Hands fill f over: its V may need special values taken out first.
     const auto hand_over = [&](int f) {
         const int j = f >> 1;
-        if (ELEM == 2 && (f & 1) && partial(j)) {
+        if (ELEM == 2 && (f & 1) && part.tile<BN>(j)) {
             unsigned char *st = sm + C::kSmRing + (f % C::kStages) * C::kStageBytes;
             for (int k = 0; k < PER; k++) {
                 const int e = tid + 128 * k, row = e / CH, c = e % CH;
@@ -389,7 +515,7 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
                 }
                 v[k] = rec < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(src + rec * D + 16 * c);
             }
-            const bool chk = (f & 1) && partial(f >> 1);
+            const bool chk = (f & 1) && part.tile<BN>(f >> 1);
 #pragma unroll
             for (int k = 0; k < PER; k++) {
                 const int e = tid + 128 * k, row = e / CH, c = e % CH;
@@ -485,7 +611,7 @@ __device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, u
             if (!role_wait(p_full + (j & 1), (j >> 1) & 1, misc, p.flags) || !have(2 * j + 1)) return;
             issue_pv<D>(tmem + C::kTmemS(j & 1), at(2 * j + 1), tmem + C::kTmemO(0), j > 0);
             mma_commit(empty + (2 * j + 1) % C::kStages);
-            mma_commit(o_done);  // phase j
+            mma_commit(o_done + (j & 1));  // phase j / 2
         }
     }
 }
@@ -521,6 +647,8 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
     const int first = last_seen(b, base, G);  // no row of the tile sees less
     const uint32_t my = tmem + ((uint32_t)(tid & ~31) << 16);
     const float scale = p.scale_log2;
+    // (The wait for s_full covers every product issued before it: with one query tile, P V of
+    // tile j - 2, so of the two o_done barriers none is more than a phase behind its wait.)
     float m = -INFINITY, sum = 0.f;  // m in units of log2: subtracted from scaled scores
     bool ok = true;
     for (int j = 0; j < b.cnt[t]; j++) {
@@ -562,7 +690,7 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
             const float mn = top <= m + kRaise ? m : top;
             const float f = m == -INFINITY ? 0.f : ex2(m - mn);
             if (j > 0) {
-                if (C::NT == 1 && !role_wait(o_done, (j - 1) & 1, misc, p.flags)) { ok = false; break; }
+                if (C::NT == 1 && !role_wait(o_done + ((j - 1) & 1), ((j - 1) >> 1) & 1, misc, p.flags)) { ok = false; break; }
                 fence_after();
                 const float f1 = mn == m ? 1.f : f;
 #pragma unroll
@@ -601,7 +729,7 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
     }
     // ---- epilogue
     if (ok && b.cnt[t] > 0) {
-        ok = role_wait(o_done + (C::NT == 2 ? t : 0), C::NT == 2 ? 0 : (b.cnt[t] - 1) & 1, misc, p.flags);
+        ok = role_wait(o_done + (C::NT == 2 ? t : (b.cnt[t] - 1) & 1), C::NT == 2 ? 0 : ((b.cnt[t] - 1) >> 1) & 1, misc, p.flags);
         fence_after();
     }
     if (!ok) return;
@@ -654,8 +782,11 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
 
 // ------------------------------------------------------------------- kernels
 
-template <int D, int ELEM>
-__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
+// TMA: a bf16 cache brought by tma_loader; else loader.
+template <int D, int ELEM, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv) {
     using C = Cfg<D>;
     extern __shared__ unsigned char smraw[];
     __shared__ Block blk;
@@ -664,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     int *bad = reinterpret_cast<int *>(sm + C::kSmBad);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kSmBar), *empty = full + C::kStages;
     uint64_t *q_full = empty + C::kStages, *s_full = q_full + 1, *p_full = s_full + 2, *o_done = p_full + 2,
-             *drain = o_done + 2;
+             *drain = o_done + 2, *land = drain + 1;
     Misc *misc = reinterpret_cast<Misc *>(sm + C::kSmMisc);
     const int warp = threadIdx.x >> 5;
     grid_dependency_wait();
@@ -676,8 +807,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     if (threadIdx.x == 32) {
         for (int i = 0; i < C::kStages; i++) {
-            mbar_init(full + i, 128);
+            mbar_init(full + i, TMA ? 1 : 128);
             mbar_init(empty + i, 1);
+            mbar_init(land + i, 1);
         }
         mbar_init(q_full, 128 * C::NT);
         mbar_init(drain, 1);
@@ -710,7 +842,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             softmax<D>(p, blk, t, p.splits > 1 ? (int64_t)blockIdx.x : -1, sm, tmem, q_full, s_full, p_full, o_done, bad, misc);
     } else if (warp < 12) {
         regs_down<72>();
-        loader<D, ELEM>(p, blk, sm, full, empty, bad, misc);
+        if (!TMA) loader<D, ELEM>(p, blk, sm, full, empty, bad, misc);
+        else if (warp == 8) tma_loader<D>(p, blk, sm, &mk, &mv, full, empty, land, misc);
+        else mender<D>(p, blk, sm, full, land, bad, misc);
     } else {
         regs_down<40>();
         if (threadIdx.x == 12 * 32) {
@@ -786,17 +920,45 @@ int splits_of(int64_t blocks, int64_t keys, int D) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sm_count(), kMostParts) / std::max<int64_t>(1, blocks), tiles / 4));
 }
 
-template <int D, int ELEM>
+// The cache as boxes of 64 dims x up to BN slots, 128-byte swizzled: [total][d], or the
+// pool's slots [L n_blocks bs][H][d] one head at a time.
+template <int D>
+bool make_map(CUtensorMap *m, const void *base, const Geometry &geo) {
+    auto fn = tensormap_encode_fn();
+    if (!fn) return false;
+    const bool paged = geo.layout == TRI_KV_PAGED;
+    const int64_t slots = paged ? (int64_t)geo.L * geo.n_blocks << geo.block_shift : geo.total;
+    const cuuint32_t box = (cuuint32_t)std::min<int64_t>(paged ? 1 << geo.block_shift : Cfg<D>::BN, Cfg<D>::BN);
+    const cuuint64_t dims3[3] = {D, (cuuint64_t)geo.H, (cuuint64_t)slots}, dims2[2] = {D, (cuuint64_t)slots};
+    const cuuint64_t str3[2] = {2 * D, (cuuint64_t)geo.H * 2 * D}, str2[1] = {2 * D};
+    const cuuint32_t box3[3] = {64, 1, box}, box2[2] = {64, box}, ones[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, paged ? 3 : 2, const_cast<void *>(base), paged ? dims3 : dims2,
+              paged ? str3 : str2, paged ? box3 : box2, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// TMA wants slot numbers of 31 bits, and pages that fill a swizzle atom of 8 rows.
+bool tma_fits(const Geometry &geo) {
+    const bool paged = geo.layout == TRI_KV_PAGED;
+    const int64_t most = 0x7fffffffLL;
+    if (paged) return geo.block_shift >= 3 && geo.n_blocks <= most / geo.L >> geo.block_shift;
+    return geo.total >= 1 && geo.total <= most;
+}
+
+template <int D, int ELEM, bool TMA>
 cudaError_t launch_t(const PrefillParams &p, int64_t units, cudaStream_t s) {
     static bool attr[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
+    auto kern = prefill_kernel<D, ELEM, TMA>;
     if (!attr[dev & 63]) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, ELEM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmem);
         if (e != cudaSuccess) return e;
         attr[dev & 63] = true;
     }
-    cudaError_t e = launch_pdl(prefill_kernel<D, ELEM>, dim3((unsigned)(units * p.splits)), dim3(kThreads), Cfg<D>::kSmem, s, p);
+    CUtensorMap mk = {}, mv = {};
+    if (TMA && (!make_map<D>(&mk, p.K, p.geo) || !make_map<D>(&mv, p.V, p.geo))) return cudaErrorInvalidValue;
+    cudaError_t e = launch_pdl(kern, dim3((unsigned)(units * p.splits)), dim3(kThreads), Cfg<D>::kSmem, s, p, mk, mv);
     if (e != cudaSuccess || p.splits == 1) return e;
     return launch_pdl(prefill_join<D>, dim3((unsigned)(units * Cfg<D>::NT * kRows / 8)), dim3(256), 0, s, p);
 }
@@ -809,7 +971,8 @@ cudaError_t launch_d(const PrefillParams &p0, cudaStream_t s) {
     const int64_t units = p.blocks * geo.L * geo.H;
     if (units > 0x7fffffffLL / 64 || p.T * geo.G > 0x7fffff00LL) return cudaErrorInvalidConfiguration;
     p.splits = splits_of(units, geo.total / ((int64_t)geo.L * geo.S * geo.H), D);
-    return geo.elem_bytes == 2 ? launch_t<D, 2>(p, units, s) : launch_t<D, 1>(p, units, s);
+    if (geo.elem_bytes == 1) return launch_t<D, 1, false>(p, units, s);
+    return tma_fits(geo) ? launch_t<D, 2, true>(p, units, s) : launch_t<D, 2, false>(p, units, s);
 }
 
 }  // namespace
