@@ -21,7 +21,7 @@
 //     only touch V tiles that some row sees in part.  fp8 caches, and blocks too
 //     small for a swizzle atom (8 slots): all four warps copy, fp8 widened to bf16
 //     (exact).
-//   - warp 12: one thread issues every product.
+//   - warp 12: issues every product.
 // Head dim 256 fits one query tile (its O takes half of tensor memory); its S is
 // double-buffered instead.
 //
@@ -185,6 +185,50 @@ __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// Two floats per register pair.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
+
+// 2^x of two values on the FMA pipe, which the softmax leaves idle while the
+// special-function unit is its bound.  x = n + f with n the nearest integer (the
+// low bits of x + 1.5 * 2^23) and f in [-1/2, 1/2]; 2^f as 1 + c1 f + .. + c4 f^4,
+// the polynomial of least maximal relative error on that interval (2.8e-6, found
+// by linear programming); n is added to its exponent.  x is held at -127, where the
+// result is exactly 0; x <= kRaise always.
+__device__ __forceinline__ void ex2_fma(f32x2 x, float &a, float &b) {
+    float lo, hi;
+    unpack2(x, lo, hi);
+    x = pack2(fmaxf(lo, -127.f), fmaxf(hi, -127.f));
+    const f32x2 r = add2(x, both(12582912.f));
+    const f32x2 f = add2(x, fma2(r, both(-1.f), both(12582912.f)));
+    f32x2 y = fma2(f, both(0.009582853876054287f), both(0.055906426161527634f));
+    y = fma2(y, f, both(0.24024099111557007f));
+    y = fma2(y, f, both(0.6931241750717163f));
+    y = fma2(y, f, both(1.f));
+    float r0, r1, y0, y1;
+    unpack2(r, r0, r1);
+    unpack2(y, y0, y1);
+    a = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23));
+    b = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23));
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t r;
@@ -538,20 +582,29 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
 
 // ------------------------------------------------------------------ products
 
+// True in one lane of a converged warp.  The warp that issues products keeps its
+// control flow uniform and elects per batch: operands then sit in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t q, uint32_t k, uint32_t d) {
     using C = Cfg<D>;
+    const uint64_t qd = smem_desc(q, 16, 1024), kd = smem_desc(k, 16, 1024);
 #pragma unroll
     for (int i = 0; i < D / 16; i++)
-        mma_ss(d, smem_desc(q + (i >> 2) * C::kSubQ + (i & 3) * 32, 16, 1024),
-               smem_desc(k + (i >> 2) * C::kSubK + (i & 3) * 32, 16, 1024), idesc(kRows, C::BN, 0), i > 0);
+        mma_ss(d, qd + (((i >> 2) * C::kSubQ + (i & 3) * 32) >> 4), kd + (((i >> 2) * C::kSubK + (i & 3) * 32) >> 4),
+               idesc(kRows, C::BN, 0), i > 0);
 }
 template <int D>
 __device__ __forceinline__ void issue_pv(uint32_t p, uint32_t v, uint32_t d, bool acc) {
     using C = Cfg<D>;
+    const uint64_t vd = smem_desc(v, C::kSubK, 1024);
 #pragma unroll
-    for (int i = 0; i < C::BN / 16; i++)
-        mma_ts(d, p + 8 * i, smem_desc(v + i * 2048, C::kSubK, 1024), idesc(kRows, D, 1), acc || i > 0);
+    for (int i = 0; i < C::BN / 16; i++) mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), idesc(kRows, D, 1), acc || i > 0);
 }
 
 template <int D>
@@ -559,7 +612,8 @@ __device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, u
                                        uint64_t *full, uint64_t *empty, uint64_t *q_full, uint64_t *s_full,
                                        uint64_t *p_full, uint64_t *o_done, Misc *misc) {
     using C = Cfg<D>;
-    const int tiles = max(b.cnt[0], b.cnt[1]);
+    const int cnt0 = b.cnt[0], cnt1 = b.cnt[1];
+    const int tiles = max(cnt0, cnt1);
     const uint32_t q = smem_u32(sm), ring = smem_u32(sm + C::kSmRing);
     const auto have = [&](int f) {
         const bool ok = role_wait(full + f % C::kStages, (f / C::kStages) & 1, misc, p.flags);
@@ -570,48 +624,69 @@ __device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, u
     if (tiles == 0 || !role_wait(q_full, 0, misc, p.flags)) return;
     if (!have(0)) return;
     if (C::NT == 2) {
-        for (int t = 0; t < 2; t++)
-            if (b.cnt[t] > 0) {
-                issue_qk<D>(q + t * C::kQBytes, at(0), tmem + C::kTmemS(t));
-                mma_commit(s_full + t);
-            }
-        mma_commit(empty);
+        if (elect_one()) {
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+                if ((t ? cnt1 : cnt0) > 0) {
+                    issue_qk<D>(q + t * C::kQBytes, at(0), tmem + C::kTmemS(t));
+                    mma_commit(s_full + t);
+                }
+            mma_commit(empty);
+        }
+        __syncwarp();
         for (int j = 0; j < tiles; j++) {
             bool v = false, k = false;  // V of tile j, K of tile j + 1 have landed
+#pragma unroll
             for (int t = 0; t < 2; t++) {
-                if (j >= b.cnt[t]) continue;
-                if (!role_wait(p_full + t, j & 1, misc, p.flags)) return;
+                const int cnt = t ? cnt1 : cnt0;
+                if (j >= cnt) continue;
                 if (!v && !have(2 * j + 1)) return;
                 v = true;
-                fence_after();
-                issue_pv<D>(tmem + C::kTmemS(t), at(2 * j + 1), tmem + C::kTmemO(t), j > 0);
-                if (j + 1 == b.cnt[t]) mma_commit(o_done + t);
-                // the last query tile that takes V
-                if (t == 1 || j >= b.cnt[1]) mma_commit(empty + (2 * j + 1) % C::kStages);
-                if (j + 1 < b.cnt[t]) {
-                    if (!k && !have(2 * j + 2)) return;
+                if (j + 1 < cnt && !k) {
+                    if (!have(2 * j + 2)) return;
                     k = true;
-                    issue_qk<D>(q + t * C::kQBytes, at(2 * j + 2), tmem + C::kTmemS(t));
-                    mma_commit(s_full + t);
-                    if (t == 1 || j + 1 >= b.cnt[1]) mma_commit(empty + (2 * j + 2) % C::kStages);
                 }
+                if (!role_wait(p_full + t, j & 1, misc, p.flags)) return;
+                fence_after();
+                if (elect_one()) {
+                    issue_pv<D>(tmem + C::kTmemS(t), at(2 * j + 1), tmem + C::kTmemO(t), j > 0);
+                    if (j + 1 == cnt) mma_commit(o_done + t);
+                    // the last query tile that takes V
+                    if (t == 1 || j >= cnt1) mma_commit(empty + (2 * j + 1) % C::kStages);
+                    if (j + 1 < cnt) {
+                        issue_qk<D>(q + t * C::kQBytes, at(2 * j + 2), tmem + C::kTmemS(t));
+                        mma_commit(s_full + t);
+                        if (t == 1 || j + 1 >= cnt1) mma_commit(empty + (2 * j + 2) % C::kStages);
+                    }
+                }
+                __syncwarp();
             }
         }
     } else {
-        issue_qk<D>(q, at(0), tmem + C::kTmemS(0));
-        mma_commit(s_full);
-        mma_commit(empty);
+        if (elect_one()) {
+            issue_qk<D>(q, at(0), tmem + C::kTmemS(0));
+            mma_commit(s_full);
+            mma_commit(empty);
+        }
+        __syncwarp();
         for (int j = 0; j < tiles; j++) {
             if (j + 1 < tiles) {
                 if (!have(2 * j + 2)) return;
-                issue_qk<D>(q, at(2 * j + 2), tmem + C::kTmemS((j + 1) & 1));
-                mma_commit(s_full + ((j + 1) & 1));
-                mma_commit(empty + (2 * j + 2) % C::kStages);
+                if (elect_one()) {
+                    issue_qk<D>(q, at(2 * j + 2), tmem + C::kTmemS((j + 1) & 1));
+                    mma_commit(s_full + ((j + 1) & 1));
+                    mma_commit(empty + (2 * j + 2) % C::kStages);
+                }
+                __syncwarp();
             }
-            if (!role_wait(p_full + (j & 1), (j >> 1) & 1, misc, p.flags) || !have(2 * j + 1)) return;
-            issue_pv<D>(tmem + C::kTmemS(j & 1), at(2 * j + 1), tmem + C::kTmemO(0), j > 0);
-            mma_commit(empty + (2 * j + 1) % C::kStages);
-            mma_commit(o_done + (j & 1));  // phase j / 2
+            if (!have(2 * j + 1) || !role_wait(p_full + (j & 1), (j >> 1) & 1, misc, p.flags)) return;
+            fence_after();
+            if (elect_one()) {
+                issue_pv<D>(tmem + C::kTmemS(j & 1), at(2 * j + 1), tmem + C::kTmemO(0), j > 0);
+                mma_commit(empty + (2 * j + 1) % C::kStages);
+                mma_commit(o_done + (j & 1));  // phase j / 2
+            }
+            __syncwarp();
         }
     }
 }
@@ -707,16 +782,24 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
             m = mn;
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const f32x2 scale2 = both(scale), off2 = both(off);
+        f32x2 part_sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < BN / 32; c++) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; k++) {
-                const float a = ex2(fmaf(__uint_as_float(s[32 * c + 2 * k]), scale, off));
-                const float d = ex2(fmaf(__uint_as_float(s[32 * c + 2 * k + 1]), scale, off));
-                part_sum[(2 * k) & 3] += a;
-                part_sum[(2 * k + 1) & 3] += d;
+                const f32x2 e = fma2(pack2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])),
+                                     scale2, off2);
+                float a, d;
+                if (k % 4 == 3) {
+                    ex2_fma(e, a, d);
+                } else {
+                    unpack2(e, a, d);
+                    a = ex2(a);
+                    d = ex2(d);
+                }
+                part_sum[k & 1] = add2(part_sum[k & 1], pack2(a, d));
                 pk[k] = bf16x2(a, d);
             }
             tmem_st16(my + C::kTmemS(sb) + 16 * c, pk);
@@ -725,7 +808,9 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + sb);
-        sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+        float s0, s1;
+        unpack2(add2(part_sum[0], part_sum[1]), s0, s1);
+        sum += s0 + s1;
     }
     // ---- epilogue
     if (ok && b.cnt[t] > 0) {
@@ -847,15 +932,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mender<D>(p, blk, sm, full, land, bad, misc);
     } else {
         regs_down<40>();
-        if (threadIdx.x == 12 * 32) {
+        if (warp == 12) {
             issuer<D>(p, blk, sm, tmem, full, empty, q_full, s_full, p_full, o_done, misc);
-            if (misc->abort_flag) {  // after a wait ran out: products in flight end before their memory is released
+            __syncwarp();
+            if (misc->abort_flag && elect_one()) {  // after a wait ran out: products in flight end before their memory is released
                 mma_commit(drain);
                 mbar_wait(drain, 0);
             }
         }
-        __syncwarp();
     }
+    __syncwarp();
     fence_before();
     __syncthreads();
     fence_after();
