@@ -9,19 +9,18 @@
 // head share its keys, so a block's rows are the (token, head) pairs of one KV head in
 // token order: a prompt of n tokens is n * G rows, cut into blocks of up to 256.
 //
-// A block (one per SM, 16 warps) computes, for its two 128-row query tiles,
+// A block (one per SM, 12 warps) computes, for its two 128-row query tiles,
 //   S = Q K^T  and  O += P V,  P = 2^(S scale log2(e) - m),
 // on tcgen05.mma (kind::f16, bf16 operands, fp32 accumulators in tensor memory):
 //   - warps 0-3 and 4-7: the softmax of query tile 0 and 1, one thread per row.  S is
 //     read from tensor memory, P (bf16) written back over it as the A operand of P V.
 //     While one tile's softmax runs, the other tile's products do.
-//   - warps 8-11: bring K and V tiles (128 keys; 64 at head dim 256) into a ring in
+//   - warps 8, 10, 11: bring K and V tiles (128 keys; 64 at head dim 256) into a ring in
 //     shared memory, 128-byte swizzled.  bf16 caches: warp 8 issues TMA copies, one
-//     box per 64 dims of a contiguous tile or of a block of pages, and warps 9-11
+//     box per 64 dims of a contiguous tile or of a block of pages, and warps 10 and 11
 //     only touch V tiles that some row sees in part.  fp8 caches, and blocks too
-//     small for a swizzle atom (8 slots): all four warps copy, fp8 widened to bf16
-//     (exact).
-//   - warp 12: issues every product.
+//     small for a swizzle atom (8 slots): all three copy, fp8 widened to bf16 (exact).
+//   - warp 9: issues every product.
 // Head dim 256 fits one query tile (its O takes half of tensor memory); its S is
 // double-buffered instead.
 //
@@ -47,7 +46,8 @@
 namespace tri {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;
+constexpr int kLoaders = 96;  // threads of warps 8, 10 and 11
 constexpr int kRows = 128;  // rows of a query tile: one per thread of a softmax warpgroup
 constexpr float kRaise = 8.f;  // log2 of the most a weight may pass 1 before the maximum is raised
 
@@ -468,14 +468,14 @@ __device__ __forceinline__ void tma_loader(const PrefillParams &p, const Block &
     }
 }
 
-// Warps 9-11 beside the TMA warp: V tiles seen in part get zeros behind the row and
+// Warps 10 and 11 beside the TMA warp: V tiles seen in part get zeros behind the row and
 // their special values taken out, then pass on to full[stage].
 template <int D>
 __device__ __forceinline__ void mender(const PrefillParams &p, const Block &b, unsigned char *sm, uint64_t *full,
                                        uint64_t *land, int *bad, Misc *misc) {
     using C = Cfg<D>;
     constexpr int BN = C::BN, CH = D / 8;
-    const int tid = threadIdx.x - 9 * 32;
+    const int tid = threadIdx.x - 10 * 32;
     const int tiles = max(b.cnt[0], b.cnt[1]);
     const Partial part(b, p.geo.G);
     uint32_t phase = 0;  // bit st: parity of land[st]
@@ -485,28 +485,29 @@ __device__ __forceinline__ void mender(const PrefillParams &p, const Block &b, u
         if (!role_wait(land + st, (phase >> st) & 1u, misc, p.flags)) break;
         phase ^= 1u << st;
         unsigned char *at = sm + C::kSmRing + st * C::kStageBytes;
-        for (int e = tid; e < BN * CH; e += 96) {
+        for (int e = tid; e < BN * CH; e += 64) {
             const int row = e / CH, c = e % CH;
             uint4 *w = reinterpret_cast<uint4 *>(at + tile_at(row, c, C::kSubK));
             if (key0 + row >= b.len) *w = make_uint4(0u, 0u, 0u, 0u);
             else if (const uint4 x = *w; has_special(x)) *w = take_out<D>(x, 8 * c, key0 + row, bad, misc);
         }
         fence_async_smem();
-        asm volatile("bar.sync 1, 96;" ::: "memory");
+        asm volatile("bar.sync 1, 64;" ::: "memory");
         if (tid == 0) mbar_arrive(full + st);
     }
 }
 
-// All four warps, for what TMA does not bring: fill 2j is K, fill 2j+1 V of key tile beg + j.  bf16 rows are copied
+// All three warps, for what TMA does not bring: fill 2j is K, fill 2j+1 V of key tile beg + j.  bf16 rows are copied
 // asynchronously, kLag fills in flight before the oldest is handed over.
 template <int D, int ELEM>
 __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, unsigned char *sm, uint64_t *full,
                                        uint64_t *empty, int *bad, Misc *misc) {
     using C = Cfg<D>;
-    constexpr int BN = C::BN, CH = D * ELEM / 16, PER = BN * CH / 128;  // 16-byte chunks per record, per thread
+    constexpr int BN = C::BN, CH = D * ELEM / 16, ALL = BN * CH;  // 16-byte chunks per record, per tile
+    constexpr int PER = (ALL + kLoaders - 1) / kLoaders;          // per thread
     constexpr int kLag = 2;
     const Geometry &geo = p.geo;
-    const int tid = threadIdx.x & 127;
+    const int tid = threadIdx.x < 288 ? threadIdx.x - 256 : threadIdx.x - 288;
     const int tiles = max(b.cnt[0], b.cnt[1]);
     const uint32_t ring = smem_u32(sm + C::kSmRing);
     const Partial part(b, geo.G);
@@ -515,8 +516,8 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
         const int j = f >> 1;
         if (ELEM == 2 && (f & 1) && part.tile<BN>(j)) {
             unsigned char *st = sm + C::kSmRing + (f % C::kStages) * C::kStageBytes;
-            for (int k = 0; k < PER; k++) {
-                const int e = tid + 128 * k, row = e / CH, c = e % CH;
+            for (int e = tid; e < ALL; e += kLoaders) {
+                const int row = e / CH, c = e % CH;
                 uint4 *at = reinterpret_cast<uint4 *>(st + tile_at(row, c, C::kSubK));
                 const uint4 v = *at;
                 if (has_special(v)) *at = take_out<D>(v, 8 * c, (b.beg + j) * BN + row, bad, misc);
@@ -532,8 +533,8 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
         const int key0 = (b.beg + (f >> 1)) * BN;
         if (ELEM == 2) {
 #pragma unroll 4
-            for (int k = 0; k < PER; k++) {
-                const int e = tid + 128 * k, row = e / CH, c = e % CH, j = key0 + row;
+            for (int e = tid; e < ALL; e += kLoaders) {
+                const int row = e / CH, c = e % CH, j = key0 + row;
                 int64_t rec = j < b.len ? record(geo, b, j) : -1;
                 if (rec < 0 && j < b.len) {
                     misc->any_missing = 1u;
@@ -551,7 +552,8 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
             uint4 v[PER];
 #pragma unroll
             for (int k = 0; k < PER; k++) {
-                const int e = tid + 128 * k, row = e / CH, c = e % CH, j = key0 + row;
+                const int e = tid + kLoaders * k, row = e / CH, c = e % CH, j = key0 + row;
+                if (e >= ALL) break;
                 const int64_t rec = j < b.len ? record(geo, b, j) : -1;
                 if (rec < 0 && j < b.len) {
                     misc->any_missing = 1u;
@@ -562,7 +564,8 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
             const bool chk = (f & 1) && part.tile<BN>(f >> 1);
 #pragma unroll
             for (int k = 0; k < PER; k++) {
-                const int e = tid + 128 * k, row = e / CH, c = e % CH;
+                const int e = tid + kLoaders * k, row = e / CH, c = e % CH;
+                if (e >= ALL) break;
                 uint4 lo = widen8(v[k].x, v[k].y), hi = widen8(v[k].z, v[k].w);
                 if (chk && has_special(lo)) lo = take_out<D>(lo, 16 * c, key0 + row, bad, misc);
                 if (chk && has_special(hi)) hi = take_out<D>(hi, 16 * c + 8, key0 + row, bad, misc);
@@ -892,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 32) {
         for (int i = 0; i < C::kStages; i++) {
-            mbar_init(full + i, TMA ? 1 : 128);
+            mbar_init(full + i, TMA ? 1 : kLoaders);
             mbar_init(empty + i, 1);
             mbar_init(land + i, 1);
         }
@@ -919,26 +922,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = misc->tmem;
-    // Registers: 512 threads are launched with 128 each; 2 x 200 + 72 + 40 = 4 x 128.
+    // Registers: 384 threads are launched with 168 each; 2 x 208 + 88 = 3 x 168.
     if (warp < 8) {
-        regs_up<200>();
+        regs_up<208>();
         const int t = warp >> 2;
         if (t < C::NT)
             softmax<D>(p, blk, t, p.splits > 1 ? (int64_t)blockIdx.x : -1, sm, tmem, q_full, s_full, p_full, o_done, bad, misc);
-    } else if (warp < 12) {
-        regs_down<72>();
-        if (!TMA) loader<D, ELEM>(p, blk, sm, full, empty, bad, misc);
-        else if (warp == 8) tma_loader<D>(p, blk, sm, &mk, &mv, full, empty, land, misc);
-        else mender<D>(p, blk, sm, full, land, bad, misc);
     } else {
-        regs_down<40>();
-        if (warp == 12) {
+        regs_down<88>();
+        if (warp == 9) {
             issuer<D>(p, blk, sm, tmem, full, empty, q_full, s_full, p_full, o_done, misc);
             __syncwarp();
             if (misc->abort_flag && elect_one()) {  // after a wait ran out: products in flight end before their memory is released
                 mma_commit(drain);
                 mbar_wait(drain, 0);
             }
+        } else if (!TMA) {
+            loader<D, ELEM>(p, blk, sm, full, empty, bad, misc);
+        } else if (warp == 8) {
+            tma_loader<D>(p, blk, sm, &mk, &mv, full, empty, land, misc);
+        } else {
+            mender<D>(p, blk, sm, full, land, bad, misc);
         }
     }
     __syncwarp();
