@@ -67,7 +67,7 @@ struct Cfg {
     static constexpr int kSmRing = NT * kQBytes;
     static constexpr int kSmBad = kSmRing + kStages * kStageBytes;  // int [3][D]
     static constexpr int kSmBar = kSmBad + 3 * D * 4;
-    static constexpr int kBars = 3 * kStages + 1 + 2 + 2 + 2 + 1;
+    static constexpr int kBars = 3 * kStages + 1 + 2 + 2 + 2 + 1 + 2;
     static constexpr int kSmMisc = kSmBar + kBars * 8;
     static constexpr size_t kSmem = kSmMisc + 64 + 1024;
 };
@@ -602,18 +602,19 @@ __device__ __forceinline__ void issue_qk(uint32_t q, uint32_t k, uint32_t d) {
         mma_ss(d, qd + (((i >> 2) * C::kSubQ + (i & 3) * 32) >> 4), kd + (((i >> 2) * C::kSubK + (i & 3) * 32) >> 4),
                idesc(kRows, C::BN, 0), i > 0);
 }
-template <int D>
+template <int D, int HALF>
 __device__ __forceinline__ void issue_pv(uint32_t p, uint32_t v, uint32_t d, bool acc) {
     using C = Cfg<D>;
     const uint64_t vd = smem_desc(v, C::kSubK, 1024);
 #pragma unroll
-    for (int i = 0; i < C::BN / 16; i++) mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), idesc(kRows, D, 1), acc || i > 0);
+    for (int i = 0; i < C::BN / 16; i++)
+        if (i / (C::BN / 32) == HALF) mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), idesc(kRows, D, 1), acc || i > 0);
 }
 
 template <int D>
 __device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, unsigned char *sm, uint32_t tmem,
                                        uint64_t *full, uint64_t *empty, uint64_t *q_full, uint64_t *s_full,
-                                       uint64_t *p_full, uint64_t *o_done, Misc *misc) {
+                                       uint64_t *p_full, uint64_t *p_half, uint64_t *o_done, Misc *misc) {
     using C = Cfg<D>;
     const int cnt0 = b.cnt[0], cnt1 = b.cnt[1];
     const int tiles = max(cnt0, cnt1);
@@ -649,10 +650,14 @@ __device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, u
                     if (!have(2 * j + 2)) return;
                     k = true;
                 }
+                if (!role_wait(p_half + t, j & 1, misc, p.flags)) return;
+                fence_after();
+                if (elect_one()) issue_pv<D, 0>(tmem + C::kTmemS(t), at(2 * j + 1), tmem + C::kTmemO(t), j > 0);
+                __syncwarp();
                 if (!role_wait(p_full + t, j & 1, misc, p.flags)) return;
                 fence_after();
                 if (elect_one()) {
-                    issue_pv<D>(tmem + C::kTmemS(t), at(2 * j + 1), tmem + C::kTmemO(t), j > 0);
+                    issue_pv<D, 1>(tmem + C::kTmemS(t), at(2 * j + 1), tmem + C::kTmemO(t), true);
                     if (j + 1 == cnt) mma_commit(o_done + t);
                     // the last query tile that takes V
                     if (t == 1 || j >= cnt1) mma_commit(empty + (2 * j + 1) % C::kStages);
@@ -682,10 +687,14 @@ __device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, u
                 }
                 __syncwarp();
             }
-            if (!have(2 * j + 1) || !role_wait(p_full + (j & 1), (j >> 1) & 1, misc, p.flags)) return;
+            if (!have(2 * j + 1) || !role_wait(p_half + (j & 1), (j >> 1) & 1, misc, p.flags)) return;
+            fence_after();
+            if (elect_one()) issue_pv<D, 0>(tmem + C::kTmemS(j & 1), at(2 * j + 1), tmem + C::kTmemO(0), j > 0);
+            __syncwarp();
+            if (!role_wait(p_full + (j & 1), (j >> 1) & 1, misc, p.flags)) return;
             fence_after();
             if (elect_one()) {
-                issue_pv<D>(tmem + C::kTmemS(j & 1), at(2 * j + 1), tmem + C::kTmemO(0), j > 0);
+                issue_pv<D, 1>(tmem + C::kTmemS(j & 1), at(2 * j + 1), tmem + C::kTmemO(0), true);
                 mma_commit(empty + (2 * j + 1) % C::kStages);
                 mma_commit(o_done + (j & 1));  // phase j / 2
             }
@@ -699,7 +708,7 @@ __device__ __forceinline__ void issuer(const PrefillParams &p, const Block &b, u
 template <int D>
 __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, int t, int64_t part, unsigned char *sm,
                                         uint32_t tmem, uint64_t *q_full, uint64_t *s_full, uint64_t *p_full,
-                                        uint64_t *o_done, const int *bad, Misc *misc) {
+                                        uint64_t *p_half, uint64_t *o_done, const int *bad, Misc *misc) {
     using C = Cfg<D>;
     constexpr int BN = C::BN;
     const Geometry &geo = p.geo;
@@ -806,6 +815,12 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
                 pk[k] = bf16x2(a, d);
             }
             tmem_st16(my + C::kTmemS(sb) + 16 * c, pk);
+            if (c == BN / 64 - 1) {
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_half + sb);
+            }
         }
         wait_st();
         fence_before();
@@ -883,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *bad = reinterpret_cast<int *>(sm + C::kSmBad);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kSmBar), *empty = full + C::kStages;
     uint64_t *q_full = empty + C::kStages, *s_full = q_full + 1, *p_full = s_full + 2, *o_done = p_full + 2,
-             *drain = o_done + 2, *land = drain + 1;
+             *drain = o_done + 2, *land = drain + 1, *p_half = land + C::kStages;
     Misc *misc = reinterpret_cast<Misc *>(sm + C::kSmMisc);
     const int warp = threadIdx.x >> 5;
     grid_dependency_wait();
@@ -904,6 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; i++) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
+            mbar_init(p_half + i, 4);
             mbar_init(o_done + i, 1);
         }
         mbar_init_fence();
@@ -927,11 +943,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_up<208>();
         const int t = warp >> 2;
         if (t < C::NT)
-            softmax<D>(p, blk, t, p.splits > 1 ? (int64_t)blockIdx.x : -1, sm, tmem, q_full, s_full, p_full, o_done, bad, misc);
+            softmax<D>(p, blk, t, p.splits > 1 ? (int64_t)blockIdx.x : -1, sm, tmem, q_full, s_full, p_full, p_half, o_done, bad, misc);
     } else {
         regs_down<88>();
         if (warp == 9) {
-            issuer<D>(p, blk, sm, tmem, full, empty, q_full, s_full, p_full, o_done, misc);
+            issuer<D>(p, blk, sm, tmem, full, empty, q_full, s_full, p_full, p_half, o_done, misc);
             __syncwarp();
             if (misc->abort_flag && elect_one()) {  // after a wait ran out: products in flight end before their memory is released
                 mma_commit(drain);
