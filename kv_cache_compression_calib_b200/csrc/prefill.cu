@@ -149,11 +149,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
 
 // -------------------------------------------------------------------- waits
 
-// Bounded wait of one role.  When it runs out the block is told to stop.
+// Bounded wait of one role (the clock is read once in 4096 tries).  When it runs out
+// the block is told to stop.
 __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Misc *misc, unsigned *flags) {
-    for (uint32_t it = 0; it < 64; it++)
+    unsigned long long t0 = 0;
+    for (uint32_t it = 1; it < kStageWaitIters; it++) {
         if (mbar_test(bar, parity)) return true;
-    if (!misc->abort_flag && mbar_wait(bar, parity)) return true;
+        if ((it & 4095u) == 0) {
+            const unsigned long long t = global_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kStageWaitNs || misc->abort_flag) break;
+        }
+    }
     misc->abort_flag = 1u;
     atomicOr(flags, TRI_FLAG_STAGE_TIMEOUT);
     return false;
@@ -248,21 +255,29 @@ struct Block {
     int64_t lo;    // row_off
     int beg;       // first key tile (of the split)
     int cnt[2];    // key tiles of each query tile, from beg
-    bool split_empty;
 };
 
+// x / G for 0 <= x < 2^31, by multiplication: mul = ceil(2^(31 + l) / G), l = ceil(log2 G).
+__device__ __forceinline__ int token_of(const PrefillParams &p, int x) {
+    return (int)(((unsigned long long)(unsigned)x * p.div_mul) >> p.div_shift);
+}
 // Last slot row x (of the sequence's rows) sees.
-__device__ __forceinline__ int last_seen(const Block &b, int x, int G) { return b.len - b.n + x / G; }
+__device__ __forceinline__ int last_seen(const PrefillParams &p, const Block &b, int x) { return b.len - b.n + token_of(p, x); }
+// Row x's place among the rows of q, out and lse.
+__device__ __forceinline__ int64_t row_of(const PrefillParams &p, const Block &b, int x) {
+    const int i = token_of(p, x);
+    return ((int64_t)b.l * p.T + b.tok0 + i) * p.geo.Hq + b.h * p.geo.G + (x - i * p.geo.G);
+}
 
 // The block's share of the work, by one warp: sequence after sequence, each cut into
 // ceil(n G / (128 NT)) blocks, the last rows (most keys) first.
 template <int D>
-__device__ __forceinline__ bool find_block(const PrefillParams &p, int64_t idx, int split, Block *out) {
+__device__ __forceinline__ bool find_block(const PrefillParams &p, int idx, int split, Block *out) {
     constexpr int R = kRows * Cfg<D>::NT, BN = Cfg<D>::BN;
     const Geometry &geo = p.geo;
     const int lane = threadIdx.x & 31;
-    const int64_t lh = idx / p.blocks;
-    int64_t b = idx % p.blocks;
+    const int lh = idx / p.blocks;
+    int b = idx - lh * p.blocks;
     for (int base = 0; base < geo.S; base += 32) {
         const int s = base + lane;
         int64_t t0 = 0, n = 0;
@@ -274,23 +289,22 @@ __device__ __forceinline__ bool find_block(const PrefillParams &p, int64_t idx, 
                 n = 0;
             }
         }
-        const int64_t mine = (n * geo.G + R - 1) / R;
-        int64_t upto = mine;
+        int upto = (int)((n * geo.G + R - 1) / R);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += x;
         }
         const uint32_t here = __ballot_sync(0xffffffffu, b < upto);
         if (here) {
             if (lane == __ffs(here) - 1) {
                 Block w;
-                w.l = (int)(lh / geo.H);
-                w.h = (int)(lh % geo.H);
+                w.l = lh / geo.H;
+                w.h = lh - w.l * geo.H;
                 w.seq = s;
                 w.n = (int)n;
                 w.rows = (int)(n * geo.G);
-                w.row0 = (int)(upto - 1 - b) * R;
+                w.row0 = (upto - 1 - b) * R;
                 w.tok0 = t0;
                 const int64_t r = ((int64_t)w.l * geo.S + s) * geo.H + w.h;
                 int64_t lo = geo.row_off[r], hi = geo.row_off[r + 1];
@@ -303,11 +317,11 @@ __device__ __forceinline__ bool find_block(const PrefillParams &p, int64_t idx, 
                 int c[2] = {0, 0};
                 for (int t = 0; t < Cfg<D>::NT; t++) {
                     const int first = w.row0 + t * kRows;
-                    if (first < w.rows) c[t] = max(0, last_seen(w, min(first + kRows, w.rows) - 1, geo.G) + BN) / BN;
+                    if (first < w.rows) c[t] = max(0, last_seen(p, w, min(first + kRows, w.rows) - 1) + BN) / BN;
                 }
                 const int all = max(c[0], c[1]);
-                w.beg = (int)((int64_t)all * split / p.splits);
-                const int end = (int)((int64_t)all * (split + 1) / p.splits);
+                w.beg = p.splits == 1 ? 0 : (int)((int64_t)all * split / p.splits);
+                const int end = p.splits == 1 ? all : (int)((int64_t)all * (split + 1) / p.splits);
                 for (int t = 0; t < 2; t++) w.cnt[t] = max(0, min(c[t], end) - w.beg);
                 *out = w;
             }
@@ -359,10 +373,14 @@ __device__ __forceinline__ uint4 take_out(uint4 v, int d0, int j, int *bad, Misc
     };
     return make_uint4(word(v.x, d0), word(v.y, d0 + 2), word(v.z, d0 + 4), word(v.w, d0 + 6));
 }
-__device__ __forceinline__ bool has_special(uint4 v) {
-    const auto one = [&](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
-    return one(v.x) || one(v.y) || one(v.z) || one(v.w);
+// Whether one of 8 bf16 values has the exponent of NaN and infinity (some bit of
+// 0x80008000): adding 1 to the exponent field then carries into the sign's place, and
+// nowhere else.
+__device__ __forceinline__ uint32_t special_bits(uint4 v) {
+    const auto one = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
+    return one(v.x) | one(v.y) | one(v.z) | one(v.w);
 }
+__device__ __forceinline__ bool has_special(uint4 v) { return (special_bits(v) & 0x80008000u) != 0; }
 
 // Eight e4m3 values (two words) as bf16.
 __device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
@@ -373,18 +391,22 @@ __device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
 // Query tile t's first row sees this many slots: key tiles past them are seen in part.
 struct Partial {
     int beg, cnt[2], first[2];
-    __device__ __forceinline__ Partial(const Block &b, int G) {
+    __device__ __forceinline__ Partial(const PrefillParams &p, const Block &b) {
         beg = b.beg;
 #pragma unroll
         for (int t = 0; t < 2; t++) {
             cnt[t] = b.cnt[t];
-            first[t] = last_seen(b, b.row0 + t * kRows, G) + 1;
+            first[t] = last_seen(p, b, b.row0 + t * kRows) + 1;
         }
     }
     template <int BN>
     __device__ __forceinline__ bool tile(int j) const {
         const int end = (beg + j + 1) * BN;
         return (j < cnt[0] && end > first[0]) || (j < cnt[1] && end > first[1]);
+    }
+    // First slot of tile j that some row does not see.
+    __device__ __forceinline__ int from(int j) const {
+        return min(j < cnt[0] ? first[0] : 0x7fffffff, j < cnt[1] ? first[1] : 0x7fffffff);
     }
 };
 
@@ -414,7 +436,7 @@ __device__ __forceinline__ void tma_loader(const PrefillParams &p, const Block &
     const int lane = threadIdx.x & 31;
     const int tiles = max(b.cnt[0], b.cnt[1]);
     const uint32_t ring = smem_u32(sm + C::kSmRing);
-    const Partial part(b, geo.G);
+    const Partial part(p, b);
     const bool paged = geo.layout == TRI_KV_PAGED;
     const int64_t lo = b.lo;
     const int len = b.len, beg = b.beg, h = b.h;
@@ -477,7 +499,7 @@ __device__ __forceinline__ void mender(const PrefillParams &p, const Block &b, u
     constexpr int BN = C::BN, CH = D / 8;
     const int tid = threadIdx.x - 10 * 32;
     const int tiles = max(b.cnt[0], b.cnt[1]);
-    const Partial part(b, p.geo.G);
+    const Partial part(p, b);
     uint32_t phase = 0;  // bit st: parity of land[st]
     for (int j = 0; j < tiles; j++) {
         if (!part.tile<BN>(j)) continue;
@@ -485,12 +507,24 @@ __device__ __forceinline__ void mender(const PrefillParams &p, const Block &b, u
         if (!role_wait(land + st, (phase >> st) & 1u, misc, p.flags)) break;
         phase ^= 1u << st;
         unsigned char *at = sm + C::kSmRing + st * C::kStageBytes;
-        for (int e = tid; e < BN * CH; e += 64) {
-            const int row = e / CH, c = e % CH;
-            uint4 *w = reinterpret_cast<uint4 *>(at + tile_at(row, c, C::kSubK));
-            if (key0 + row >= b.len) *w = make_uint4(0u, 0u, 0u, 0u);
-            else if (const uint4 x = *w; has_special(x)) *w = take_out<D>(x, 8 * c, key0 + row, bad, misc);
+        const auto chunk = [&](int e) { return reinterpret_cast<uint4 *>(at + tile_at(e / CH, e % CH, C::kSubK)); };
+        // Only slots that some row does not see, eight chunks of a thread at once; behind the
+        // row's end, zeros.
+        constexpr int BATCH = 8;
+        const int stop = min(BN, b.len - key0) * CH;
+        for (int e0 = max(0, part.from(j) - key0) * CH + tid; e0 < stop; e0 += 64 * BATCH) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int k = 0; k < BATCH; k++)
+                if (e0 + 64 * k < stop) any |= special_bits(*chunk(e0 + 64 * k));
+            if (any & 0x80008000u) {
+#pragma unroll 1
+                for (int e = e0; e < min(stop, e0 + 64 * BATCH); e += 64)
+                    if (special_bits(*chunk(e)) & 0x80008000u)
+                        *chunk(e) = take_out<D>(*chunk(e), 8 * (e % CH), key0 + e / CH, bad, misc);
+            }
         }
+        for (int e = stop + tid; e < BN * CH; e += 64) *chunk(e) = make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
         asm volatile("bar.sync 1, 64;" ::: "memory");
         if (tid == 0) mbar_arrive(full + st);
@@ -510,7 +544,7 @@ __device__ __forceinline__ void loader(const PrefillParams &p, const Block &b, u
     const int tid = threadIdx.x < 288 ? threadIdx.x - 256 : threadIdx.x - 288;
     const int tiles = max(b.cnt[0], b.cnt[1]);
     const uint32_t ring = smem_u32(sm + C::kSmRing);
-    const Partial part(b, geo.G);
+    const Partial part(p, b);
     // Hands fill f over: its V may need special values taken out first.
     const auto hand_over = [&](int f) {
         const int j = f >> 1;
@@ -713,16 +747,26 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
     constexpr int BN = C::BN;
     const Geometry &geo = p.geo;
     const int tid = threadIdx.x & 127, lane = tid & 31;
-    const int G = geo.G;
     const int base = b.row0 + t * kRows;  // first row of the tile
-    // The query tile: 16-byte chunks, rows behind the sequence's last as zeros.
-    for (int e = tid; e < kRows * D / 8; e += 128) {
-        const int row = e / (D / 8), c = e % (D / 8), x = base + row;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (x < b.rows)
-            v = *reinterpret_cast<const uint4 *>(
-                p.q + (((int64_t)b.l * p.T + b.tok0 + x / G) * geo.Hq + b.h * G + x % G) * D + 8 * c);
-        *reinterpret_cast<uint4 *>(sm + t * C::kQBytes + tile_at(row, c, C::kSubQ)) = v;
+    // The query tile: 16-byte chunks, rows behind the sequence's last as zeros; a thread's
+    // loads are all issued before the first is stored.
+    {
+        constexpr int CH = D / 8, PER = kRows * CH / 128, BATCH = PER < 16 ? PER : 16;
+#pragma unroll
+        for (int k0 = 0; k0 < PER; k0 += BATCH) {
+            uint4 v[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; k++) {
+                const int e = tid + 128 * (k0 + k), x = base + e / CH;
+                v[k] = x < b.rows ? *reinterpret_cast<const uint4 *>(p.q + row_of(p, b, x) * D + 8 * (e % CH))
+                                  : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; k++) {
+                const int e = tid + 128 * (k0 + k);
+                *reinterpret_cast<uint4 *>(sm + t * C::kQBytes + tile_at(e / CH, e % CH, C::kSubQ)) = v[k];
+            }
+        }
     }
     fence_async_smem();
     mbar_arrive(q_full);
@@ -730,8 +774,8 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
     const int x = base + tid;
     const bool real = x < b.rows;
     // rows behind the last see what the last does; they are not written
-    const int limit = last_seen(b, min(x, b.rows - 1), G);
-    const int first = last_seen(b, base, G);  // no row of the tile sees less
+    const int limit = last_seen(p, b, min(x, b.rows - 1));
+    const int first = last_seen(p, b, base);  // no row of the tile sees less
     const uint32_t my = tmem + ((uint32_t)(tid & ~31) << 16);
     const float scale = p.scale_log2;
     // (The wait for s_full covers every product issued before it: with one query tile, P V of
@@ -838,7 +882,7 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
     if (!ok) return;
     const bool nothing = sum == 0.f;
     const float inv = nothing ? 0.f : 1.f / sum;
-    const int64_t row = ((int64_t)b.l * p.T + b.tok0 + x / G) * geo.Hq + b.h * G + x % G;
+    const int64_t row = row_of(p, b, min(x, b.rows - 1));
     if (part < 0 && real && p.lse) p.lse[row] = nothing ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
     float *slab = p.part + part * (C::NT * kRows) * (D + 2) + (t * kRows + tid) * (D + 2);
     if (part >= 0) {
@@ -869,15 +913,28 @@ __device__ __forceinline__ void softmax(const PrefillParams &p, const Block &b, 
 #pragma unroll
             for (int k = 0; k < 32; k += 2)
                 *reinterpret_cast<uint2 *>(slab + 32 * c + k) = make_uint2(o[k], o[k + 1]);
-        } else if (real) {
-            uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * D + 32 * c);
+        } else {
+            // through the query tile, which no product reads any more: rows of a warp are
+            // its own, and go out as whole 16-byte runs of consecutive rows below
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 const auto two = [&](int i) {
                     return bf16x2(__uint_as_float(o[8 * k + i]) * inv, __uint_as_float(o[8 * k + i + 1]) * inv);
                 };
-                dst[k] = make_uint4(two(0), two(2), two(4), two(6));
+                *reinterpret_cast<uint4 *>(sm + t * C::kQBytes + tile_at(tid, 4 * c + k, C::kSubQ)) =
+                    make_uint4(two(0), two(2), two(4), two(6));
             }
+        }
+    }
+    if (part < 0) {
+        constexpr int CH = D / 8;
+        __syncwarp();
+#pragma unroll 8
+        for (int e = lane; e < 32 * CH; e += 32) {
+            const int r = (tid & ~31) + e / CH;
+            if (base + r < b.rows)
+                *reinterpret_cast<uint4 *>(p.out + row_of(p, b, base + r) * D + 8 * (e % CH)) =
+                    *reinterpret_cast<const uint4 *>(sm + t * C::kQBytes + tile_at(r, e % CH, C::kSubQ));
         }
     }
     fence_before();
@@ -902,8 +959,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc *misc = reinterpret_cast<Misc *>(sm + C::kSmMisc);
     const int warp = threadIdx.x >> 5;
     grid_dependency_wait();
-    const int split = (int)(blockIdx.x % p.splits);
-    const int64_t idx = blockIdx.x / p.splits;
+    const int idx = p.splits == 1 ? blockIdx.x : blockIdx.x / p.splits;
+    const int split = (int)blockIdx.x - idx * p.splits;
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&misc->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     if (warp == 0) {
         const bool f = find_block<D>(p, idx, split, &blk);
         if ((threadIdx.x & 31) == 0) found = f;
@@ -928,16 +989,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         misc->any_missing = 0u;
     }
     for (int e = threadIdx.x; e < 3 * D; e += kThreads) bad[e] = 0x7fffffff;
-    __syncthreads();
-    if (!found) return;
-    if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&misc->tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = misc->tmem;
+    if (found) {
     // Registers: 384 threads are launched with 168 each; 2 x 208 + 88 = 3 x 168.
     if (warp < 8) {
         regs_up<208>();
@@ -965,6 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
+    }
     if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     grid_dependents_launch();
 }
@@ -977,9 +1034,8 @@ __global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ Pref
     __shared__ Block blk;
     __shared__ int found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Geometry &geo = p.geo;
     grid_dependency_wait();
-    const int64_t idx = blockIdx.x / PER;
+    const int idx = blockIdx.x / PER;
     const int r = (int)(blockIdx.x % PER) * 8 + warp;
     if (warp == 0) {
         const bool f = find_block<D>(p, idx, 0, &blk);
@@ -988,7 +1044,7 @@ __global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ Pref
     __syncthreads();
     const int x = blk.row0 + r;
     if (!found || x >= blk.rows) return;
-    const float *slab = p.part + idx * p.splits * (int64_t)R * (D + 2) + (int64_t)r * (D + 2);
+    const float *slab = p.part + (int64_t)idx * p.splits * R * (D + 2) + (int64_t)r * (D + 2);
     float m = -INFINITY;
     for (int k = 0; k < p.splits; k++) m = max2(m, slab[(int64_t)k * R * (D + 2) + D]);
     float sum = 0.f, o[D / 32] = {0.f};
@@ -1001,7 +1057,7 @@ __global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ Pref
 #pragma unroll
         for (int e = 0; e < D / 32; e++) o[e] = fmaf(w, s[lane + 32 * e], o[e]);
     }
-    const int64_t row = ((int64_t)blk.l * p.T + blk.tok0 + x / geo.G) * geo.Hq + blk.h * geo.G + x % geo.G;
+    const int64_t row = row_of(p, blk, x);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int e = 0; e < D / 32; e++) {
@@ -1073,8 +1129,12 @@ template <int D>
 cudaError_t launch_d(const PrefillParams &p0, cudaStream_t s) {
     PrefillParams p = p0;
     const Geometry &geo = p.geo;
-    p.blocks = most_blocks(geo.S, geo.G, D, p.T);
-    const int64_t units = p.blocks * geo.L * geo.H;
+    const int64_t blocks = most_blocks(geo.S, geo.G, D, p.T), units = blocks * geo.L * geo.H;
+    p.blocks = (int32_t)blocks;
+    int l = 0;
+    while ((1 << l) < geo.G) l++;
+    p.div_shift = 31 + l;
+    p.div_mul = ((1ull << (31 + l)) + geo.G - 1) / geo.G;
     if (units > 0x7fffffffLL / 64 || p.T * geo.G > 0x7fffff00LL) return cudaErrorInvalidConfiguration;
     p.splits = splits_of(units, geo.total / ((int64_t)geo.L * geo.S * geo.H), D);
     if (geo.elem_bytes == 1) return launch_t<D, 1, false>(p, units, s);

@@ -167,8 +167,11 @@ struct PrefillParams {
     float *lse;         // [L][T][Hq] or null
     float *part;        // scratch of split rows
     unsigned *flags;
-    int64_t blocks;  // bound of the blocks per (layer, KV head), set at launch
-    int32_t splits;  // parts each row's keys are cut into, set at launch
+    // set at launch:
+    int32_t blocks;  // bound of the blocks per (layer, KV head)
+    int32_t splits;  // parts each row's keys are cut into
+    unsigned long long div_mul;  // division by G
+    int32_t div_shift;
 };
 
 constexpr int kFusedMaxRow = TRI_FUSED_MAX_ROW;  // longest row the fused score-and-select kernel holds on chip
