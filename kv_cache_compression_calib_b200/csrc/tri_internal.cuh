@@ -172,6 +172,7 @@ struct PrefillParams {
     int32_t splits;  // parts each row's keys are cut into
     unsigned long long div_mul;  // division by G
     int32_t div_shift;
+    int32_t q_tma;  // queries come by TMA
 };
 
 constexpr int kFusedMaxRow = TRI_FUSED_MAX_ROW;  // longest row the fused score-and-select kernel holds on chip
