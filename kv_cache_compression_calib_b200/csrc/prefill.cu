@@ -78,9 +78,8 @@ struct Cfg {
     // shared memory from a 1024-byte aligned base
     static constexpr int kSmRing = NT * kQBytes;
     static constexpr int kSmRaw = kSmRing + kStages * kStageBytes;
-    static constexpr int kSmOut = kSmRaw + kRaws * kRawBytes;  // 2 KB per softmax warp
-    static constexpr int kSmBad = kSmOut + 4 * NT * 2048;      // int [kSlots][3][D]
-    static constexpr int kSmMisc = kSmBad + kSlots * 3 * D * 4;
+    static constexpr int kSmBad = kSmRaw + kRaws * kRawBytes;  // int [3][D]
+    static constexpr int kSmMisc = kSmBad + 3 * D * 4;
 };
 
 template <int STAGES, int RAWS>
@@ -90,7 +89,7 @@ struct Shared {
     uint64_t raw_full[RAWS + 1], raw_empty[RAWS + 1];
     uint64_t q_full, q_empty, claimed, drain;
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];
-    uint64_t item_full[kSlots], item_empty[kSlots];
+    uint64_t item_full[kSlots], item_empty[kSlots], scanned[kSlots];
 };
 
 struct Misc {
@@ -132,6 +131,7 @@ struct Block {
     int place;     // of its part, where rows are split
     volatile uint32_t any_bad;      // a NaN or infinite value of V was taken out
     volatile uint32_t any_missing;  // a slot without a block
+    volatile uint32_t mend;         // V tiles seen in part hold NaN or infinities
     __device__ __forceinline__ int tiles() const { return max(cnt[0], cnt[1]); }
 };
 
@@ -330,7 +330,8 @@ struct Ctx {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(sh->item_empty + n % kSlots);
     }
-    __device__ __forceinline__ int *bad(int n) const { return reinterpret_cast<int *>(sm + C::kSmBad) + (n % kSlots) * 3 * D; }
+    // Per dim, the first slot whose V is NaN, +inf, -inf there (any_bad of the item says whether any is).
+    __device__ __forceinline__ int *bad() const { return reinterpret_cast<int *>(sm + C::kSmBad); }
     __device__ __forceinline__ unsigned char *stage(int f) const { return sm + C::kSmRing + (f % C::kStages) * C::kStageBytes; }
 };
 
@@ -368,13 +369,9 @@ template <int D, int SRC>
 __device__ __forceinline__ bool next_item(const Ctx<D, SRC> &c, int n, int *claims) {
     const int lane = threadIdx.x & 31;
     Block *b = c.slots + n % kSlots;
-    if (n >= kSlots) {
-        if (!c.wait(c.sh->item_empty + n % kSlots, n / kSlots - 1)) return false;
-        if (b->any_bad)
-            for (int e = lane; e < 3 * D; e += 32) c.bad(n)[e] = 0x7fffffff;
-    }
+    if (n >= kSlots && !c.wait(c.sh->item_empty + n % kSlots, n / kSlots - 1)) return false;
     __syncwarp();
-    if (lane == 0) b->any_bad = b->any_missing = 0u;
+    if (lane == 0) b->any_bad = b->any_missing = b->mend = 0u;
     int idx = n == 0 ? (int)blockIdx.x : claim_block(c, claims);
     bool found = false;
     while (idx >= 0) {  // the blocks of the grid are a bound: some name no item
@@ -394,9 +391,11 @@ __device__ __forceinline__ bool next_item(const Ctx<D, SRC> &c, int n, int *clai
 
 // -------------------------------------------------------------------- loading
 
-// Warp 8 with TMA.  Fill 2j of an item is K, fill 2j+1 V of its key tile beg + j.  A
-// V tile of a bf16 cache that is seen in part lands on land[stage], for the mending
-// warps; fp8 tiles land in the raw ring, for the widening ones.
+// Warp 8 with TMA.  Fill 2j of an item is K, fill 2j+1 V of its key tile beg + j.  Where
+// the scan found NaN or infinities, V tiles that are seen in part land on land[stage],
+// for the mending warps; fp8 tiles land in the raw ring, for the widening ones.  Pages
+// behind the row's end, or that the table does not name, are asked for behind the end of
+// the pool, where a copy delivers zeros.
 template <int D, int SRC>
 __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap *mk, const CUtensorMap *mv, const CUtensorMap *mq) {
     using C = Cfg<D, SRC>;
@@ -407,6 +406,7 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
     const int lane = threadIdx.x & 31;
     const bool paged = geo.layout == TRI_KV_PAGED;
     const int box = paged ? min(1 << geo.block_shift, BN) : BN;  // slots per copy
+    const int pool_end = (int)(paged ? (int64_t)geo.L * geo.n_blocks << geo.block_shift : geo.total);
     int fill = 0;
     for (int n = 0;; n++) {
         Block *b = c.item(n);
@@ -436,35 +436,29 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
                 constexpr int RING = RAW ? C::kRaws : C::kStages;
                 const int st = f % RING, round = f / RING;
                 if (round > 0 && !c.wait(RAW ? c.sh->raw_empty + st : c.sh->empty + st, round - 1)) return;
-                uint64_t *bar = RAW ? c.sh->raw_full + st : v && part.tile<BN>(g >> 1) ? c.sh->land + st : c.sh->full + st;
-                unsigned char *dst = RAW ? c.sm + C::kSmRaw + st * C::kRawBytes : c.stage(f);
-                const uint32_t here = __ballot_sync(0xffffffffu, slot >= 0);
-                if (here != __ballot_sync(0xffffffffu, mine)) {  // blocks that the table does not name
-                    b->any_missing = 1u;
-                    if (mine && slot < 0) {
-                        atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
-                        // no weight reaches their keys; their values must be finite
-                        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                        if (RAW)
-                            for (int e = 0; e < box * D / 16; e++) *reinterpret_cast<uint4 *>(dst + lane * box * D + e * 16) = zero;
-                        else
-                            for (int x = 0; x < D / 64; x++)
-                                for (int e = 0; e < box * 8; e++)
-                                    *reinterpret_cast<uint4 *>(dst + x * C::kSubK + lane * box * 128 + e * 16) = zero;
-                    }
-                    fence_async_smem();
-                    __syncwarp();
+                bool mend = false;
+                if (!RAW && v && part.tile<BN>(g >> 1)) {
+                    if (!c.wait(c.sh->scanned + n % kSlots, n / kSlots)) return;
+                    mend = b->mend;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(here) * box * D * (RAW ? 1 : 2)));
+                uint64_t *bar = RAW ? c.sh->raw_full + st : mend ? c.sh->land + st : c.sh->full + st;
+                const uint32_t dst = smem_u32(RAW ? c.sm + C::kSmRaw + st * C::kRawBytes : c.stage(f));
+                if (mine && slot < 0) {  // a block that the table does not name
+                    b->any_missing = 1u;
+                    atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
+                }
                 __syncwarp();
-                if (slot >= 0) {
+                if (lane == 0) mbar_arrive_expect_tx(bar, RAW ? C::kRawBytes : C::kStageBytes);
+                __syncwarp();
+                if (lane * box < BN) {
                     const CUtensorMap *map = v ? mv : mk;
+                    const int at = slot < 0 ? pool_end : (int)slot;
                     if (RAW) {
-                        tma_rows(smem_u32(dst) + lane * box * D, map, paged, 0, h, (int)slot, bar);
+                        tma_rows(dst + lane * box * D, map, paged, 0, h, at, bar);
                     } else {
 #pragma unroll
                         for (int x = 0; x < D / 64; x++)
-                            tma_rows(smem_u32(dst) + x * C::kSubK + lane * box * 128, map, paged, 64 * x, h, (int)slot, bar);
+                            tma_rows(dst + x * C::kSubK + lane * box * 128, map, paged, 64 * x, h, at, bar);
                     }
                 }
             }
@@ -482,6 +476,34 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
         }
         fill += 2 * tiles;
         c.leave(n);
+    }
+}
+
+// Warps 10 and 11 for one item of a bf16 cache, ahead of its copies: whether the slots
+// that some row does not see, up to the end of the last tile as the copies bring it, hold
+// NaN or infinite values of V.  Read from global memory: the copies then find them in L2, and
+// shared memory, whose bandwidth the products take, is left alone.
+template <int D, int SRC>
+__device__ __forceinline__ void scan(const Ctx<D, SRC> &c, Block *b) {
+    constexpr int BN = Cfg<D, SRC>::BN, CH = D / 8, BATCH = 8;
+    const Geometry &geo = c.p.geo;
+    const int tid = threadIdx.x - 10 * 32;
+    const Partial part(c.p, *b);
+    const int stop = (b->beg + b->tiles()) * BN, len = b->len;
+    const int start = max(b->beg * BN, min(b->cnt[0] > 0 ? part.first[0] : stop, b->cnt[1] > 0 ? part.first[1] : stop));
+    const bool paged = geo.layout == TRI_KV_PAGED;
+    const int box = paged ? min(1 << geo.block_shift, BN) : BN;
+    const int there = paged ? min(stop, (len + box - 1) & -box) : (int)min((int64_t)stop, geo.total - b->lo);
+#pragma unroll 1
+    for (int e0 = start * CH + tid; e0 < there * CH; e0 += 64 * BATCH) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int k = 0; k < BATCH; k++) {
+            const int e = e0 + 64 * k;
+            const int64_t rec = e < there * CH ? record(geo, *b, e / CH) : -1;
+            if (rec >= 0) any |= special_bits(*reinterpret_cast<const uint4 *>(c.p.V + (rec * CH + e % CH) * 16));
+        }
+        if (any & 0x80008000u) b->mend = 1u;
     }
 }
 
@@ -664,16 +686,36 @@ __device__ __forceinline__ void fill_warps(const Ctx<D, SRC> &c) {
     uint32_t phase = 0;
     bool more = warp == 10 && next_item(c, 0, &claims);
     for (int n = 0;; n++) {
-        if (more) more = next_item(c, n + 1, &claims);
+        // An item is claimed while the one before it runs, not earlier: blocks that are
+        // still free should have it.
+        if (SRC != kTma16 && more) more = next_item(c, n + 1, &claims);
         Block *b = c.item(n);
         if (!b) return;
-        int *bad = c.bad(n);
+        int *bad = c.bad();
         bool ok;
-        if constexpr (SRC == kTma16) ok = mend(c, b, bad, fill, &phase);
-        else if constexpr (SRC == kTma8) ok = widen(c, b, bad, fill);
-        else ok = copy(c, b, bad, fill);
+        if (n > 0 && c.slots[(n - 1) % kSlots].any_bad) {  // the notes are the last item's until its epilogue is done
+            if (!c.wait(c.sh->item_empty + (n - 1) % kSlots, (n - 1) / kSlots)) return;
+            __syncwarp();
+            for (int e = threadIdx.x & 31; e < 3 * D; e += 32) bad[e] = 0x7fffffff;
+            asm volatile("bar.sync 1, %0;" ::"n"(Cfg<D, SRC>::kLoaders) : "memory");
+        }
+        if constexpr (SRC == kTma16) {
+            scan(c, b);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(c.sh->scanned + n % kSlots);
+            ok = c.wait(c.sh->scanned + n % kSlots, n / kSlots) && (!b->mend || mend(c, b, bad, fill, &phase));
+            if (ok && more) {
+                if (n > 0) ok = c.wait(c.sh->item_empty + (n - 1) % kSlots, (n - 1) / kSlots);
+                more = ok && next_item(c, n + 1, &claims);
+            }
+        } else if constexpr (SRC == kTma8) {
+            ok = widen(c, b, bad, fill);
+        } else {
+            ok = copy(c, b, bad, fill);
+        }
         if (!ok) return;
         fill += 2 * b->tiles();
+        asm volatile("bar.sync 1, %0;" ::"n"(Cfg<D, SRC>::kLoaders) : "memory");  // any_bad is final
         c.leave(n);
     }
 }
@@ -821,6 +863,18 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
 }
 
 // -------------------------------------------------------------------- softmax
+
+// 32 bytes to global memory: one store where the address is a multiple of 32.
+__device__ __forceinline__ void st32(char *to, const uint32_t *w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(to + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 
 // Rows of a part: O [kRowsPer][D] fp32, then (m, sum) [kRowsPer].
 template <class C, int D>
@@ -985,31 +1039,10 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
     } else if (p.lse && x < b.rows) {
         p.lse[row_of(p, b, x)] = nothing ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
     }
-    // A warp's rows go out through 2 KB of its own, 64 bytes of each of its 32 rows at a time: lane
-    // l then writes 16 bytes of rows l / 4, l / 4 + 8, ...
-    unsigned char *stg = c.sm + C::kSmOut + (threadIdx.x >> 5) * 2048;
-    const int row0 = base + (tid & ~31);
-    char *to[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const int r = row0 + 8 * k + (lane >> 2);
-        to[k] = parts ? (char *)(part_of<C, D>(p, b.place) + (r - b.row0) * D)
-                : r < b.rows ? (char *)(p.out + row_of(p, b, r) * D) : nullptr;
-    }
-    const auto flush = [&](const uint32_t (&w)[16], int off) {  // 64 bytes of each row, from byte `off` of it
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            *reinterpret_cast<uint4 *>(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const int r = 8 * k + (lane >> 2);
-            const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-            if (to[k]) *reinterpret_cast<uint4 *>(to[k] + off + 16 * (lane & 3)) = v;
-        }
-        __syncwarp();
-    };
+    // Each thread writes its own row, 32 bytes (a sector) at a time where the row allows:
+    // going through shared memory for whole lines was slower beside the other tile's products.
+    char *to = parts ? (char *)(part_of<C, D>(p, b.place) + (t * kRows + tid) * D) : (char *)(p.out + row_of(p, b, min(x, b.rows - 1)) * D);
+    const bool wide = ((uintptr_t)(parts ? (const void *)p.part : (const void *)p.out) & 31) == 0;
     const bool fix = b.any_bad && cnt > 0;
 #pragma unroll 1
     for (int k0 = 0; k0 < D; k0 += 32) {
@@ -1035,20 +1068,18 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
                 if (at[k] <= limit) o[k] = 0x7fc00000u;
             }
         }
-        uint32_t w[16];
         if (parts) {
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-#pragma unroll
-                for (int e = 0; e < 16; e++) w[e] = o[16 * h + e];
-                flush(w, (k0 + 16 * h) * 4);
-            }
-        } else {
+            for (int e = 0; e < 32; e += 8) st32(to + (k0 + e) * 4, o + e, wide);
+        } else if (x < b.rows) {
+            uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; e++)
                 w[e] = bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-            flush(w, k0 * 2);
+            st32(to + k0 * 2, w, wide);
+            st32(to + k0 * 2 + 32, w + 8, wide);
         }
+        __syncwarp();
     }
     return true;
 }
@@ -1095,12 +1126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kSlots; i++) {
             mbar_init(sh.item_full + i, 1);
+            mbar_init(sh.scanned + i, 2);
             mbar_init(sh.item_empty + i, 4 * C::NT + 4);  // the softmax warps and warps 8 to 11
         }
         mbar_init_fence();
         misc.abort_flag = 0u;
     }
-    for (int e = threadIdx.x; e < kSlots * 3 * D; e += kThreads) reinterpret_cast<int *>(sm + C::kSmBad)[e] = 0x7fffffff;
+    for (int e = threadIdx.x; e < 3 * D; e += kThreads) reinterpret_cast<int *>(sm + C::kSmBad)[e] = 0x7fffffff;
     fence_before();
     __syncthreads();
     fence_after();
@@ -1115,7 +1147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0;; n++) {
                 Block *b = c.item(n);
                 if (!b) break;
-                if (!softmax(c, *b, c.bad(n), t, n, before, outs)) break;
+                if (!softmax(c, *b, c.bad(), t, n, before, outs)) break;
                 before += b->cnt[t];
                 outs += b->cnt[t] > 0;
                 c.leave(n);
