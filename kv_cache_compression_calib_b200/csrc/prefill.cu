@@ -769,9 +769,9 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
         if (!have(fill)) return;
         if (C::NT == 2) {
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < 2; t++)
-                    if (cnt[t] > 0) {
+                    if ((t ? cnt[1] : cnt[0]) > 0) {
                         issue_qk<C, D>(q + t * C::kQBytes, at(fill), tmem + C::kTmemS(t));
                         mma_commit(c.sh->s_full + t);
                     }
@@ -782,10 +782,11 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
             for (int j = 0; j < tiles; j++) {
                 const int fv = fill + 2 * j + 1, fk = fv + 1;
                 bool v = false, k = false;  // V of tile j, K of tile j + 1 have landed
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < 2; t++) {
-                    if (j >= cnt[t]) continue;
-                    const bool more = j + 1 < cnt[t];
+                    const int mine = t ? cnt[1] : cnt[0], before = t ? done[1] : done[0], used = t ? outs[1] : outs[0];
+                    if (j >= mine) continue;
+                    const bool more = j + 1 < mine;
                     if (!v && !have(fv)) return;
                     v = true;
                     if (more && !k) {
@@ -793,12 +794,12 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
                         k = true;
                     }
                     // the epilogue before has read this tile's O
-                    if (j == 0 && outs[t] > 0 && !c.wait(c.sh->o_free + t, outs[t] - 1)) return;
-                    if (!c.wait(c.sh->p_half + t, done[t] + j)) return;
+                    if (j == 0 && used > 0 && !c.wait(c.sh->o_free + t, used - 1)) return;
+                    if (!c.wait(c.sh->p_half + t, before + j)) return;
                     fence_after();
                     if (elect_one()) issue_pv<C, D, 0>(tmem + C::kTmemS(t), at(fv), tmem + C::kTmemO(t), j > 0);
                     __syncwarp();
-                    if (!c.wait(c.sh->p_full + t, done[t] + j)) return;
+                    if (!c.wait(c.sh->p_full + t, before + j)) return;
                     fence_after();
                     if (elect_one()) {
                         issue_pv<C, D, 1>(tmem + C::kTmemS(t), at(fv), tmem + C::kTmemO(t), true);
@@ -952,17 +953,25 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
             }
             wait_st();
         }
-        uint32_t s[BN];
-#pragma unroll
-        for (int k = 0; k < BN / 32; k++) tmem_ld32(my + C::kTmemS(sb) + 32 * k, s + 32 * k);
-        wait_ld();
+        // The upper half of the keys, then the lower one, which stays in registers for the
+        // weights; the upper half is read again after them.  (The weights' code is a loop of
+        // two turns: unrolled over all keys it outgrew the instruction cache beside the other
+        // warps' code, and a tenth of the warps' time went into fetching.)
+        constexpr int HALF = BN / 2;
+        uint32_t s[HALF];
         float mx[4];
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            constexpr int W = BN / 4;
-            mx[q] = max2(__uint_as_float(s[q * W]), __uint_as_float(s[q * W + 1]));
+        for (int h = 1; h >= 0; h--) {
 #pragma unroll
-            for (int k = 2; k < W; k += 2) mx[q] = max3(mx[q], __uint_as_float(s[q * W + k]), __uint_as_float(s[q * W + k + 1]));
+            for (int k = 0; k < HALF; k += 32) tmem_ld32(my + C::kTmemS(sb) + HALF * h + k, s + k);
+            wait_ld();
+#pragma unroll
+            for (int k = 0; k < HALF; k += 8)
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const float u = __uint_as_float(s[k + 2 * q]), v = __uint_as_float(s[k + 2 * q + 1]);
+                    mx[q] = h == 1 && k == 0 ? max2(u, v) : max3(mx[q], u, v);
+                }
         }
         float top = max2(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
         if (top == INFINITY) top = NAN;  // inf - inf, as the definition has it
@@ -989,13 +998,12 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
         const float off = m == -INFINITY ? 0.f : -m;
         const f32x2 scale2 = both(scale), off2 = both(off);
         f32x2 part_sum[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int h = 0; h < 2; h++) {
+            uint32_t pk[HALF / 2];
 #pragma unroll
-        for (int q = 0; q < BN / 32; q++) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; k++) {
-                const f32x2 e = fma2(pack2(__uint_as_float(s[32 * q + 2 * k]), __uint_as_float(s[32 * q + 2 * k + 1])),
-                                     scale2, off2);
+            for (int k = 0; k < HALF / 2; k++) {
+                const f32x2 e = fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, off2);
                 float a, d;
                 if (k % 4 == 3) {
                     ex2_fma(e, a, d);
@@ -1007,18 +1015,20 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
                 part_sum[k & 1] = add2(part_sum[k & 1], pack2(a, d));
                 pk[k] = bf16x2(a, d);
             }
-            tmem_st16(my + C::kTmemS(sb) + 16 * q, pk);
-            if (q == BN / 64 - 1) {
-                wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(c.sh->p_half + sb);
+            // P of the lower half lies over S of the lower quarter, P of the upper half over the
+            // rest of the lower half: S of the upper half stays until it is read
+            if (HALF == 64) tmem_st32(my + C::kTmemS(sb) + 32 * h, pk);
+            else tmem_st16(my + C::kTmemS(sb) + 16 * h, pk);
+            if (h == 0) {
+#pragma unroll
+                for (int k = 0; k < HALF; k += 32) tmem_ld32(my + C::kTmemS(sb) + HALF + k, s + k);
             }
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive((h == 0 ? c.sh->p_half : c.sh->p_full) + sb);
+            if (h == 0) wait_ld();
         }
-        wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c.sh->p_full + sb);
         float s0, s1;
         unpack2(add2(part_sum[0], part_sum[1]), s0, s1);
         sum += s0 + s1;
