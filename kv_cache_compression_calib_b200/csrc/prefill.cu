@@ -14,7 +14,8 @@
 //
 // For an item's two 128-row query tiles it computes
 //   S = Q K^T  and  O += P V,  P = 2^(S scale log2(e) - m),
-// on tcgen05.mma (kind::f16, bf16 operands, fp32 accumulators in tensor memory):
+// on tcgen05.mma (kind::f16, bf16 operands - fp16 where the cache is fp8, below - and fp32
+// accumulators in tensor memory):
 //   - warps 0-3 and 4-7: the softmax of query tile 0 and 1, one thread per row.  S is
 //     read from tensor memory, P (bf16) written back over it as the A operand of P V,
 //     which starts on the first half of the keys while the second half's weights are
@@ -24,10 +25,17 @@
 //     dims of a contiguous tile or of a page.  It runs ahead into the next item.
 //   - warp 9: issues every product.
 //   - warps 10 and 11: see to V tiles that some row sees in part (below), and widen fp8
-//     tiles (exactly) to bf16 from a second ring; warp 10 also finds the next item.
+//     tiles to fp16 from a second ring; warp 10 also finds the next item.
 //     Pages of fewer than 8 slots (a swizzle atom) are copied by warps 8, 10 and 11.
 // Head dim 256 fits one query tile (its O takes half of tensor memory); its S is
 // double-buffered instead.
+//
+// fp8 caches: e4m3 widens to fp16 by one conversion per two values (to bf16 it takes
+// five instructions), exactly.  The queries then have to be fp16 as well: a row is
+// scaled by the power of two that brings its largest value to [2^14, 2^15), which its
+// score scale takes back, so values down to 2^-31 of the largest keep all eight bits of
+// their bf16.  P is fp16, too: weights of at most 2^8 keep eleven bits, and those below
+// 2^-14 an absolute 2^-25.
 //
 // The maximum m a row subtracts is only raised when its scores pass it by more than
 // 2^8 (weights up to 256 lose nothing in bf16 or fp32), so O is rescaled rarely.
@@ -71,6 +79,7 @@ struct Cfg {
     static constexpr int kQBytes = kRows * D * 2;  // per query tile
     static constexpr int kSubQ = kRows * 128;      // a 64-dim column of a Q tile
     static constexpr int kSubK = BN * 128;         // ... of a K or V tile
+    static constexpr bool kF16 = SRC == kTma8 || SRC == kCopy8;  // fp16 operands
     static constexpr int kLoaders = SRC >= kCopy16 ? 96 : 64;  // threads of the loading warps that fill or mend
     // tensor memory columns
     static constexpr int kTmemS(int b) { return b * BN; }  // S (and P) of tile b, or buffer b
@@ -259,10 +268,38 @@ __device__ __forceinline__ uint32_t special_bits(uint4 v) {
 }
 __device__ __forceinline__ bool has_special(uint4 v) { return (special_bits(v) & 0x80008000u) != 0; }
 
-// Eight e4m3 values (two words) as bf16.
-__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
-    const float2 x = e4m3x2_to_float2(a), y = e4m3x2_to_float2(a >> 16), z = e4m3x2_to_float2(b), w = e4m3x2_to_float2(b >> 16);
-    return make_uint4(bf16x2(x.x, x.y), bf16x2(y.x, y.y), bf16x2(z.x, z.y), bf16x2(w.x, w.y));
+// Four e4m3 values as fp16 (exact; NaN stays NaN).
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    uint2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(w));
+    return r;
+}
+// 16 e4m3 values of a tile's row as two chunks of fp16.
+__device__ __forceinline__ void widen16(uint4 v, unsigned char *tile, int row, int ch, int sub) {
+    const uint2 a = widen4(v.x), b = widen4(v.y), c = widen4(v.z), d = widen4(v.w);
+    *reinterpret_cast<uint4 *>(tile + tile_at(row, 2 * ch, sub)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4 *>(tile + tile_at(row, 2 * ch + 1, sub)) = make_uint4(c.x, c.y, d.x, d.y);
+}
+// Whether one of 16 e4m3 values is NaN.
+__device__ __forceinline__ bool has_nan8(uint4 v) {
+    const auto one = [](uint32_t x) { return (x & 0x7f7f7f7fu) + 0x01010101u; };
+    return ((one(v.x) | one(v.y) | one(v.z) | one(v.w)) & 0x80808080u) != 0;
+}
+// take_out for 16 e4m3 values (which have no infinities).
+__device__ __forceinline__ uint4 take_out8(uint4 v, int d0, int j, int *bad, Block *b) {
+    b->any_bad = 1u;
+    const auto word = [&](uint32_t w, int d) {
+#pragma unroll 1
+        for (int k = 0; k < 4; k++)
+            if ((w >> (8 * k) & 0x7fu) == 0x7fu) {
+                atomicMin(bad + d + k, j);
+                w &= ~(0xffu << (8 * k));
+            }
+        return w;
+    };
+    return make_uint4(word(v.x, d0), word(v.y, d0 + 4), word(v.z, d0 + 8), word(v.w, d0 + 12));
 }
 
 // Query tile t's first row sees this many slots: key tiles past them are seen in part.
@@ -546,21 +583,7 @@ __device__ __forceinline__ bool mend(const Ctx<D, SRC> &c, Block *b, int *bad, i
     return true;
 }
 
-// Two e4m3 values (bytes 1 and 3 of x, zeros elsewhere) as bf16: sign, exponent and
-// mantissa moved into place read as 2^-120 of the value, e4m3's subnormals as bf16's;
-// the product with 2^120 is exact.  NaN codes are not seen to here.
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {
-    const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));
-    return r;
-}
-__device__ __forceinline__ bool has_nan8(uint4 v) {
-    const auto one = [](uint32_t x) { return (x & 0x7f7f7f7fu) + 0x01010101u; };
-    return ((one(v.x) | one(v.y) | one(v.z) | one(v.w)) & 0x80808080u) != 0;
-}
-
-// Warps 10 and 11 for one item of an fp8 cache: every tile from the raw ring to bf16.
+// Warps 10 and 11 for one item of an fp8 cache: every tile from the raw ring to fp16.
 template <int D, int SRC>
 __device__ __forceinline__ bool widen(const Ctx<D, SRC> &c, Block *b, int *bad, int fill) {
     using C = Cfg<D, SRC>;
@@ -575,31 +598,24 @@ __device__ __forceinline__ bool widen(const Ctx<D, SRC> &c, Block *b, int *bad, 
         const bool check = (g & 1) && part.tile<BN>(g >> 1);
         const unsigned char *from = c.sm + C::kSmRaw + raw * C::kRawBytes;
         unsigned char *to = c.stage(f);
-        constexpr int BATCH = 4;
+        constexpr int BATCH = 8;
 #pragma unroll 1
         for (int e0 = tid; e0 < BN * CH; e0 += 64 * BATCH) {
             uint4 v[BATCH];
 #pragma unroll
             for (int k = 0; k < BATCH; k++) v[k] = *reinterpret_cast<const uint4 *>(from + 16 * (e0 + 64 * k));
+            if (check) {
+#pragma unroll
+                for (int k = 0; k < BATCH; k++) {
+                    const int e = e0 + 64 * k, j = key0 + e / CH;
+                    if (j >= len) v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    else if (has_nan8(v[k])) v[k] = take_out8(v[k], 16 * (e % CH), j, bad, b);
+                }
+            }
 #pragma unroll
             for (int k = 0; k < BATCH; k++) {
-                const int e = e0 + 64 * k, row = e / CH, ch = e % CH;
-                uint4 lo = make_uint4(widen2(__byte_perm(v[k].x, 0, 0x1404)), widen2(__byte_perm(v[k].x, 0, 0x3424)),
-                                      widen2(__byte_perm(v[k].y, 0, 0x1404)), widen2(__byte_perm(v[k].y, 0, 0x3424)));
-                uint4 hi = make_uint4(widen2(__byte_perm(v[k].z, 0, 0x1404)), widen2(__byte_perm(v[k].z, 0, 0x3424)),
-                                      widen2(__byte_perm(v[k].w, 0, 0x1404)), widen2(__byte_perm(v[k].w, 0, 0x3424)));
-                if (check && key0 + row >= len) {
-                    lo = hi = make_uint4(0u, 0u, 0u, 0u);
-                } else if (has_nan8(v[k])) {
-                    lo = widen8(v[k].x, v[k].y);
-                    hi = widen8(v[k].z, v[k].w);
-                    if (check) {
-                        lo = take_out<D>(lo, 16 * ch, key0 + row, bad, b);
-                        hi = take_out<D>(hi, 16 * ch + 8, key0 + row, bad, b);
-                    }
-                }
-                *reinterpret_cast<uint4 *>(to + tile_at(row, 2 * ch, C::kSubK)) = lo;
-                *reinterpret_cast<uint4 *>(to + tile_at(row, 2 * ch + 1, C::kSubK)) = hi;
+                const int e = e0 + 64 * k;
+                widen16(v[k], to, e / CH, e % CH, C::kSubK);
             }
         }
         fence_async_smem();
@@ -652,12 +668,9 @@ __device__ __forceinline__ bool copy(const Ctx<D, SRC> &c, Block *b, int *bad, i
             if (ELEM == 2) {
                 cp16(smem_u32(c.stage(f) + tile_at(row, ch, C::kSubK)), src + (rec < 0 ? 0 : rec) * (2 * D) + 16 * ch, rec >= 0);
             } else {
-                const uint4 v = rec < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(src + rec * D + 16 * ch);
-                uint4 lo = widen8(v.x, v.y), hi = widen8(v.z, v.w);
-                if (check && has_special(lo)) lo = take_out<D>(lo, 16 * ch, j, bad, b);
-                if (check && has_special(hi)) hi = take_out<D>(hi, 16 * ch + 8, j, bad, b);
-                *reinterpret_cast<uint4 *>(c.stage(f) + tile_at(row, 2 * ch, C::kSubK)) = lo;
-                *reinterpret_cast<uint4 *>(c.stage(f) + tile_at(row, 2 * ch + 1, C::kSubK)) = hi;
+                uint4 v = rec < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(src + rec * D + 16 * ch);
+                if (check && has_nan8(v)) v = take_out8(v, 16 * ch, j, bad, b);
+                widen16(v, c.stage(f), row, ch, C::kSubK);
             }
         }
         if (ELEM == 2) {
@@ -728,7 +741,7 @@ __device__ __forceinline__ void issue_qk(uint32_t q, uint32_t k, uint32_t d) {
 #pragma unroll
     for (int i = 0; i < D / 16; i++)
         mma_ss(d, qd + (((i >> 2) * C::kSubQ + (i & 3) * 32) >> 4), kd + (((i >> 2) * C::kSubK + (i & 3) * 32) >> 4),
-               idesc(kRows, C::BN, 0), i > 0);
+               idesc(kRows, C::BN, 0, !C::kF16), i > 0);
 }
 // The product with V over one half of a tile's keys.
 template <class C, int D, int HALF>
@@ -737,7 +750,7 @@ __device__ __forceinline__ void issue_pv(uint32_t p, uint32_t v, uint32_t d, boo
     constexpr int K = C::BN / 32;
 #pragma unroll
     for (int i = HALF * K; i < (HALF + 1) * K; i++)
-        mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), idesc(kRows, D, 1), acc || i > 0);
+        mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), idesc(kRows, D, 1, !C::kF16), acc || i > 0);
 }
 
 template <int D, int SRC>
@@ -893,7 +906,46 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
     const Geometry &geo = p.geo;
     const int tid = threadIdx.x & 127, lane = tid & 31;
     const int base = b.row0 + t * kRows;  // first row of the tile
-    if (!p.q_tma) {
+    const int x = base + tid;
+    float scale = p.scale_log2;
+    if (C::kF16) {
+        // The thread's own row as fp16, scaled by a power of two: one pass for the largest
+        // magnitude, one to convert.
+        constexpr int CH = D / 8, BATCH = 8;
+        const uint4 *row = reinterpret_cast<const uint4 *>(p.q + row_of(p, b, min(x, b.rows - 1)) * D);
+        uint32_t top = 0;
+#pragma unroll 1
+        for (int k0 = 0; k0 < CH; k0 += BATCH) {
+            uint4 v[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; k++) v[k] = row[k0 + k];
+#pragma unroll
+            for (int k = 0; k < BATCH; k++)
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+        }
+        // exponent field of the largest; up is 2^(127 + 14 - field) in two factors that never overflow
+        const int field = (int)(max(top & 0xffffu, top >> 16) >> 7);
+        const bool plain = field == 0 || field == 255;  // nothing but zeros and subnormals, or NaN and infinity
+        const int up = plain ? 0 : 141 - field;
+        const float f1 = __uint_as_float((uint32_t)(127 + up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+        scale = scale / f1 / f2;
+        if (n > 0 && !c.wait(&c.sh->q_empty, n - 1)) return false;
+#pragma unroll 1
+        for (int k0 = 0; k0 < CH; k0 += BATCH) {
+            uint4 v[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; k++) v[k] = row[k0 + k];
+#pragma unroll
+            for (int k = 0; k < BATCH; k++) {
+                const auto two = [&](uint32_t w) { return f16x2(bf16lo(w) * f1 * f2, bf16hi(w) * f1 * f2); };
+                *reinterpret_cast<uint4 *>(c.sm + t * C::kQBytes + tile_at(tid, k0 + k, C::kSubQ)) =
+                    make_uint4(two(v[k].x), two(v[k].y), two(v[k].z), two(v[k].w));
+            }
+        }
+        fence_async_smem();
+        mbar_arrive(&c.sh->q_full);
+    } else if (!p.q_tma) {
         // The query tile: 16-byte chunks, rows behind the sequence's last as zeros; a thread's
         // loads are all issued before the first is stored.
         constexpr int CH = D / 8, PER = kRows * CH / 128, BATCH = PER < 16 ? PER : 16;
@@ -917,13 +969,11 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
         mbar_arrive(&c.sh->q_full);
     }
 
-    const int x = base + tid;
     // rows behind the last see what the last does; they are not written
     const int limit = last_seen(p, b, min(x, b.rows - 1));
     const int first = last_seen(p, b, base);  // no row of the tile sees less
     const int cnt = b.cnt[t], beg = b.beg;
     const uint32_t my = c.tmem + ((uint32_t)(tid & ~31) << 16);
-    const float scale = p.scale_log2;
     // (The wait for s_full covers every product issued before it: with one query tile, P V of
     // tile j - 2, so of the two o_done barriers none is more than a phase behind its wait.)
     float m = -INFINITY, sum = 0.f;  // m in units of log2: subtracted from scaled scores
@@ -1013,7 +1063,7 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
                     d = ex2(d);
                 }
                 part_sum[k & 1] = add2(part_sum[k & 1], pack2(a, d));
-                pk[k] = bf16x2(a, d);
+                pk[k] = C::kF16 ? f16x2(a, d) : bf16x2(a, d);
             }
             // P of the lower half lies over S of the lower quarter, P of the upper half over the
             // rest of the lower half: S of the upper half stays until it is read
@@ -1299,7 +1349,7 @@ cudaError_t launch_t(PrefillParams p, int64_t units, cudaStream_t s) {
     }
     CUtensorMap mk = {}, mv = {}, mq = {};
     if (SRC < kCopy16 && (!make_map<D, SRC>(&mk, p.K, p.geo) || !make_map<D, SRC>(&mv, p.V, p.geo))) return cudaErrorInvalidValue;
-    p.q_tma = SRC < kCopy16 && kRows % p.geo.G == 0 && p.geo.L * p.T <= 0x7fffffffLL;
+    p.q_tma = SRC == kTma16 && kRows % p.geo.G == 0 && p.geo.L * p.T <= 0x7fffffffLL;
     if (p.q_tma && !make_q_map<D>(&mq, p)) return cudaErrorInvalidValue;
     cudaError_t e = launch_pdl(kern, dim3((unsigned)(units * p.splits)), dim3(kThreads), smem, s, p, mk, mv, mq);
     if (e != cudaSuccess || p.splits == 1) return e;

@@ -14,9 +14,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// kind::f16 instruction descriptor: fp32 accumulator, bf16 A and B, B K-major or MN-major.
-constexpr uint32_t idesc(int M, int N, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+// kind::f16 instruction descriptor: fp32 accumulator, A and B both bf16 or both fp16, B
+// K-major or MN-major.
+constexpr uint32_t idesc(int M, int N, int b_mn, bool bf16 = true) {
+    return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
 
@@ -140,6 +141,11 @@ __device__ __forceinline__ void ex2_fma(f32x2 x, float &a, float &b) {
     unpack2(y, y0, y1);
     a = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23));
     b = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23));
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t r;
