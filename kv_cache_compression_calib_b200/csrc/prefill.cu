@@ -46,6 +46,11 @@
 // only in part, NaN and infinite values of V are taken out and noted per dim; the
 // epilogue gives them back to the rows that see them.
 //
+// An item of at most 128 rows leaves the second query tile empty: both softmax
+// warpgroups then take the same rows, one the even key tiles and one the odd ones, and the
+// first merges the two (a "twin" item; one token over a 2K row waits on the chain product -
+// softmax - product, not on memory).
+//
 // When the items are fewer than the SMs, each row is split over its keys, and
 // prefill_join merges the parts.  Every wait is bounded.
 #include <algorithm>
@@ -88,7 +93,8 @@ struct Cfg {
     static constexpr int kSmRing = NT * kQBytes;
     static constexpr int kSmRaw = kSmRing + kStages * kStageBytes;
     static constexpr int kSmBad = kSmRaw + kRaws * kRawBytes;  // int [3][D]
-    static constexpr int kSmMisc = kSmBad + 3 * D * 4;
+    static constexpr int kSmTwin = kSmBad + 3 * D * 4;         // float2 [kRows]
+    static constexpr int kSmMisc = kSmTwin + kRows * 8;
 };
 
 template <int STAGES, int RAWS>
@@ -96,7 +102,7 @@ struct Shared {
     alignas(16) uint4 claim;  // cluster launch control's answer
     uint64_t full[STAGES], empty[STAGES], land[STAGES];
     uint64_t raw_full[RAWS + 1], raw_empty[RAWS + 1];
-    uint64_t q_full, q_empty, claimed, drain;
+    uint64_t q_full, q_empty, claimed, drain, twin_done;
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];
     uint64_t item_full[kSlots], item_empty[kSlots], scanned[kSlots];
 };
@@ -136,12 +142,13 @@ struct Block {
     int64_t tok0;  // tok_off[seq]
     int64_t lo;    // row_off
     int beg;       // first key tile (of the split)
-    int cnt[2];    // key tiles of each query tile, from beg
+    int cnt[2];    // key tiles of each query tile, from beg; of a twin item, of each half
+    int twin;      // both query tiles are the same rows, tile t taking key tiles t, t + 2, ...
     int place;     // of its part, where rows are split
     volatile uint32_t any_bad;      // a NaN or infinite value of V was taken out
     volatile uint32_t any_missing;  // a slot without a block
     volatile uint32_t mend;         // V tiles seen in part hold NaN or infinities
-    __device__ __forceinline__ int tiles() const { return max(cnt[0], cnt[1]); }
+    __device__ __forceinline__ int tiles() const { return twin ? cnt[0] + cnt[1] : max(cnt[0], cnt[1]); }
 };
 
 // x / G for 0 <= x < 2^31, by multiplication: mul = ceil(2^(31 + l) / G), l = ceil(log2 G).
@@ -210,6 +217,11 @@ __device__ __forceinline__ bool find_block(const PrefillParams &p, int idx, int 
                 w.beg = p.splits == 1 ? 0 : (int)((int64_t)all * split / p.splits);
                 const int end = p.splits == 1 ? all : (int)((int64_t)all * (split + 1) / p.splits);
                 for (int t = 0; t < 2; t++) w.cnt[t] = max(0, min(c[t], end) - w.beg);
+                w.twin = Cfg<D, 0>::NT == 2 && w.row0 + kRows >= w.rows;
+                if (w.twin) {
+                    w.cnt[1] = w.cnt[0] / 2;
+                    w.cnt[0] -= w.cnt[1];
+                }
             }
             if (idx == 0)  // the first block looks at the offsets of the sequences behind its own, too
                 for (int x = s + 32; x < geo.S; x += 32)
@@ -309,7 +321,7 @@ struct Partial {
         beg = b.beg;
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            cnt[t] = b.cnt[t];
+            cnt[t] = b.twin ? (t ? 0 : b.tiles()) : b.cnt[t];
             first[t] = last_seen(p, b, b.row0 + t * kRows) + 1;
         }
     }
@@ -443,6 +455,7 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
     const int lane = threadIdx.x & 31;
     const bool paged = geo.layout == TRI_KV_PAGED;
     const int box = paged ? min(1 << geo.block_shift, BN) : BN;  // slots per copy
+    constexpr int kNone = -1, kMissing = -2;
     const int pool_end = (int)(paged ? (int64_t)geo.L * geo.n_blocks << geo.block_shift : geo.total);
     int fill = 0;
     for (int n = 0;; n++) {
@@ -452,23 +465,24 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
         const int tiles = b->tiles(), len = b->len, beg = b->beg, h = b->h;
         const int64_t lo = b->lo, layer = (int64_t)b->l * geo.n_blocks;
         const int32_t *table = geo.block_table + (int64_t)b->seq * geo.max_blocks;
+        // Slot of the pool that a copy starts at for slot j of the row.
+        const auto slot_of = [&](int j) -> int {
+            if (lane * box >= BN || j >= len) return kNone;
+            if (!paged) return (int)(lo + j);
+            const int bi = j >> geo.block_shift;
+            const int32_t blk = bi < geo.max_blocks ? __ldg(table + bi) : -1;
+            if (blk < 0 || blk >= geo.n_blocks) return kMissing;  // a block that the table does not name
+            return (int)(((layer + blk) << geo.block_shift) + (j & ((1 << geo.block_shift) - 1)));
+        };
+        int slot = kNone, next = slot_of(beg * BN + lane * box);
         const int total = max(1, 2 * tiles);  // an item without keys still has its queries
         for (int g = 0; g < total; g++) {
             if (g < 2 * tiles) {
                 const int f = fill + g;
                 const bool v = g & 1;
-                const int key0 = (beg + (g >> 1)) * BN;
-                // Slot of the pool that the lane's copy starts at (looked up before the wait below).
-                int64_t slot = -1;
-                const int j = key0 + lane * box;
-                const bool mine = lane * box < BN && j < len;
-                if (paged && mine) {
-                    const int bi = j >> geo.block_shift;
-                    const int32_t blk = bi < geo.max_blocks ? __ldg(table + bi) : -1;
-                    if (blk >= 0 && blk < geo.n_blocks)
-                        slot = ((layer + blk) << geo.block_shift) + (j & ((1 << geo.block_shift) - 1));
-                } else if (mine) {
-                    slot = lo + j;
+                if (!v) {  // K and V of a tile come from the same slots; the next tile's are looked up meanwhile
+                    slot = next;
+                    next = g + 2 < 2 * tiles ? slot_of((beg + (g >> 1) + 1) * BN + lane * box) : kNone;
                 }
                 constexpr int RING = RAW ? C::kRaws : C::kStages;
                 const int st = f % RING, round = f / RING;
@@ -480,7 +494,7 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
                 }
                 uint64_t *bar = RAW ? c.sh->raw_full + st : mend ? c.sh->land + st : c.sh->full + st;
                 const uint32_t dst = smem_u32(RAW ? c.sm + C::kSmRaw + st * C::kRawBytes : c.stage(f));
-                if (mine && slot < 0) {  // a block that the table does not name
+                if (slot == kMissing) {
                     b->any_missing = 1u;
                     atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
                 }
@@ -489,7 +503,7 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
                 __syncwarp();
                 if (lane * box < BN) {
                     const CUtensorMap *map = v ? mv : mk;
-                    const int at = slot < 0 ? pool_end : (int)slot;
+                    const int at = slot < 0 ? pool_end : slot;
                     if (RAW) {
                         tma_rows(dst + lane * box * D, map, paged, 0, h, at, bar);
                     } else {
@@ -527,7 +541,7 @@ __device__ __forceinline__ void scan(const Ctx<D, SRC> &c, Block *b) {
     const int tid = threadIdx.x - 10 * 32;
     const Partial part(c.p, *b);
     const int stop = (b->beg + b->tiles()) * BN, len = b->len;
-    const int start = max(b->beg * BN, min(b->cnt[0] > 0 ? part.first[0] : stop, b->cnt[1] > 0 ? part.first[1] : stop));
+    const int start = max(b->beg * BN, min(part.cnt[0] > 0 ? part.first[0] : stop, part.cnt[1] > 0 ? part.first[1] : stop));
     const bool paged = geo.layout == TRI_KV_PAGED;
     const int box = paged ? min(1 << geo.block_shift, BN) : BN;
     const int there = paged ? min(stop, (len + box - 1) & -box) : (int)min((int64_t)stop, geo.total - b->lo);
@@ -771,7 +785,8 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
         const Block *b = c.item(n);
         if (!b) return;
         const int cnt[2] = {b->cnt[0], b->cnt[1]};
-        const int tiles = max(cnt[0], cnt[1]);
+        const int tiles = b->tiles();
+        const bool twin = C::NT == 2 && b->twin;
         c.leave(n);
         if (!c.wait(&c.sh->q_full, n)) return;
         if (tiles == 0) {
@@ -780,7 +795,47 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
             continue;
         }
         if (!have(fill)) return;
-        if (C::NT == 2) {
+        if (twin) {
+            // key tile j for query tile j & 1; the query rows are those of tile 0
+            for (int j = 0; j < min(2, tiles); j++) {
+                if (!have(fill + 2 * j)) return;
+                if (elect_one()) {
+                    issue_qk<C, D>(q, at(fill + 2 * j), tmem + C::kTmemS(j));
+                    mma_commit(c.sh->s_full + j);
+                    release(fill + 2 * j);
+                    if (j + 1 == tiles) mma_commit(&c.sh->q_empty);
+                }
+                __syncwarp();
+            }
+            for (int j = 0; j < tiles; j++) {
+                const int t = j & 1, fv = fill + 2 * j + 1, fk = fv + 3;
+                const int before = t ? done[1] : done[0], used = t ? outs[1] : outs[0];
+                if (!have(fv)) return;
+                if (j < 2 && used > 0 && !c.wait(c.sh->o_free + t, used - 1)) return;
+                if (!c.wait(c.sh->p_half + t, before + (j >> 1))) return;
+                fence_after();
+                if (elect_one()) issue_pv<C, D, 0>(tmem + C::kTmemS(t), at(fv), tmem + C::kTmemO(t), j > 1);
+                __syncwarp();
+                if (!c.wait(c.sh->p_full + t, before + (j >> 1))) return;
+                fence_after();
+                if (elect_one()) {
+                    issue_pv<C, D, 1>(tmem + C::kTmemS(t), at(fv), tmem + C::kTmemO(t), true);
+                    if (j + 2 >= tiles) mma_commit(c.sh->o_done + t);
+                    release(fv);
+                }
+                __syncwarp();
+                if (j + 2 < tiles) {
+                    if (!have(fk)) return;
+                    if (elect_one()) {
+                        issue_qk<C, D>(q, at(fk), tmem + C::kTmemS(t));
+                        mma_commit(c.sh->s_full + t);
+                        release(fk);
+                        if (j + 3 == tiles) mma_commit(&c.sh->q_empty);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (C::NT == 2) {
             if (elect_one()) {
 #pragma unroll 1
                 for (int t = 0; t < 2; t++)
@@ -899,13 +954,15 @@ __device__ __forceinline__ float *part_of(const PrefillParams &p, int64_t place)
 // One item's softmax of query tile t.  `before`: key tiles of this query tile in the
 // items before, `outs`: items with any.
 template <int D, int SRC>
-__device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, const int *bad, int t, int n, int before, int outs) {
+__device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, const int *bad, int t, int n, int before, int outs,
+                                        int *twins) {
     using C = Cfg<D, SRC>;
     constexpr int BN = C::BN;
     const PrefillParams &p = c.p;
     const Geometry &geo = p.geo;
     const int tid = threadIdx.x & 127, lane = tid & 31;
-    const int base = b.row0 + t * kRows;  // first row of the tile
+    const bool twin = C::NT == 2 && b.twin;
+    const int base = b.row0 + (twin ? 0 : t * kRows);  // first row of the tile
     const int x = base + tid;
     float scale = p.scale_log2;
     if (C::kF16) {
@@ -972,7 +1029,7 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
     // rows behind the last see what the last does; they are not written
     const int limit = last_seen(p, b, min(x, b.rows - 1));
     const int first = last_seen(p, b, base);  // no row of the tile sees less
-    const int cnt = b.cnt[t], beg = b.beg;
+    const int cnt = b.cnt[t], beg = b.beg + (twin ? t : 0), step = twin ? 2 : 1;
     const uint32_t my = c.tmem + ((uint32_t)(tid & ~31) << 16);
     // (The wait for s_full covers every product issued before it: with one query tile, P V of
     // tile j - 2, so of the two o_done barriers none is more than a phase behind its wait.)
@@ -982,7 +1039,7 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
         const int sb = C::NT == 2 ? t : at & 1;
         if (!c.wait(c.sh->s_full + sb, C::NT == 2 ? at : at >> 1)) return false;
         fence_after();
-        const int key0 = (beg + j) * BN;
+        const int key0 = (beg + j * step) * BN;
         const bool missing = b.any_missing;
         if (key0 + BN - 1 > first || missing) {
             // Some row sees the tile only in part, or slots have no block: minus infinity goes to
@@ -1089,11 +1146,36 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
         if (!c.wait(c.sh->o_done + (C::NT == 2 ? t : at & 1), C::NT == 2 ? outs : at >> 1)) return false;
         fence_after();
     }
+    // A twin item: the second warpgroup leaves its statistics and its O to the first.
+    float f0 = 1.f, f1 = 0.f;  // what O of query tile t, and of the twin, is worth
+    const bool join = twin && b.cnt[1] > 0;
+    if (join) {
+        float2 *notes = reinterpret_cast<float2 *>(c.sm + C::kSmTwin) + tid;
+        if (t == 1) {
+            *notes = make_float2(m, sum);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.sh->twin_done);
+            return true;
+        }
+        if (!c.wait(&c.sh->twin_done, (*twins)++)) return false;
+        fence_after();
+        const float2 o = *notes;
+        const float mn = max2(m, o.x);
+        f0 = m == -INFINITY ? 0.f : ex2(m - mn);
+        f1 = o.x == -INFINITY ? 0.f : ex2(o.x - mn);
+        sum = sum * f0 + o.y * f1;
+        m = mn;
+    } else if (twin && t == 1) {
+        return true;
+    }
     const bool nothing = sum == 0.f;
     const bool parts = p.splits > 1;
     const float inv = parts ? 1.f : nothing ? 0.f : 1.f / sum;
+    f0 *= inv;
+    f1 *= inv;
     if (parts) {
-        float *ml = part_of<C, D>(p, b.place) + C::kRowsPer * D + 2 * (t * kRows + tid);
+        float *ml = part_of<C, D>(p, b.place) + C::kRowsPer * D + 2 * (x - b.row0);
         ml[0] = nothing ? -INFINITY : m;
         ml[1] = sum;
     } else if (p.lse && x < b.rows) {
@@ -1101,7 +1183,8 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
     }
     // Each thread writes its own row, 32 bytes (a sector) at a time where the row allows:
     // going through shared memory for whole lines was slower beside the other tile's products.
-    char *to = parts ? (char *)(part_of<C, D>(p, b.place) + (t * kRows + tid) * D) : (char *)(p.out + row_of(p, b, min(x, b.rows - 1)) * D);
+    char *to = parts ? (char *)(part_of<C, D>(p, b.place) + (x - b.row0) * D)
+                     : (char *)(p.out + row_of(p, b, min(x, b.rows - 1)) * D);
     const bool wide = ((uintptr_t)(parts ? (const void *)p.part : (const void *)p.out) & 31) == 0;
     const bool fix = b.any_bad && cnt > 0;
 #pragma unroll 1
@@ -1110,10 +1193,22 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
         if (cnt > 0) {
             tmem_ld32(my + C::kTmemO(t) + k0, o);
             wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+            if (join) {
+                uint32_t o1[32];
+                tmem_ld32(my + C::kTmemO(1) + k0, o1);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e++) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
+            }
             if (k0 == D - 32) {  // O is free for the next item
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(c.sh->o_free + t);
+                if (lane == 0) {
+                    mbar_arrive(c.sh->o_free + t);
+                    if (join) mbar_arrive(c.sh->o_free + 1);
+                }
             }
         } else {
 #pragma unroll
@@ -1135,7 +1230,7 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC> &c, const Block &b, co
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; e++)
-                w[e] = bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                w[e] = bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
             st32(to + k0 * 2, w, wide);
             st32(to + k0 * 2 + 32, w + 8, wide);
         }
@@ -1177,6 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.claimed, 1);
         mbar_init(&sh.drain, 1);
+        mbar_init(&sh.twin_done, 4);
         for (int i = 0; i < 2; i++) {
             mbar_init(sh.s_full + i, 1);
             mbar_init(sh.p_half + i, 4);
@@ -1203,11 +1299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_up<208>();
         const int t = warp >> 2;
         if (t < C::NT) {
-            int before = 0, outs = 0;
+            int before = 0, outs = 0, twins = 0;
             for (int n = 0;; n++) {
                 Block *b = c.item(n);
                 if (!b) break;
-                if (!softmax(c, *b, c.bad(), t, n, before, outs)) break;
+                if (!softmax(c, *b, c.bad(), t, n, before, outs, &twins)) break;
                 before += b->cnt[t];
                 outs += b->cnt[t] > 0;
                 c.leave(n);
