@@ -314,6 +314,20 @@ __device__ __forceinline__ uint4 take_out8(uint4 v, int d0, int j, int *bad, Blo
     return make_uint4(word(v.x, d0), word(v.y, d0 + 4), word(v.z, d0 + 8), word(v.w, d0 + 12));
 }
 
+// The order in which an item's key tiles are brought: K_0, then K_{j+1} before V_j, and
+// the last V.  V_j is held until its weights are formed and used; behind it, K_{j+1}
+// would come a copy's latency too late where one tile's chain of steps is the bound.
+__device__ __forceinline__ int k_fill(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_fill(int j, int tiles) { return j + 1 < tiles ? 2 * j + 2 : 2 * tiles - 1; }
+struct Fill {
+    int tile;
+    bool v;
+    __device__ __forceinline__ Fill(int g, int tiles) {
+        v = g == 2 * tiles - 1 || (g > 0 && g % 2 == 0);
+        tile = g == 2 * tiles - 1 ? tiles - 1 : v ? g / 2 - 1 : (g + 1) / 2;
+    }
+};
+
 // Query tile t's first row sees this many slots: key tiles past them are seen in part.
 struct Partial {
     int beg, cnt[2], first[2];
@@ -440,8 +454,7 @@ __device__ __forceinline__ bool next_item(const Ctx<D, SRC> &c, int n, int *clai
 
 // -------------------------------------------------------------------- loading
 
-// Warp 8 with TMA.  Fill 2j of an item is K, fill 2j+1 V of its key tile beg + j.  Where
-// the scan found NaN or infinities, V tiles that are seen in part land on land[stage],
+// Warp 8 with TMA.  Where the scan found NaN or infinities, V tiles that are seen in part land on land[stage],
 // for the mending warps; fp8 tiles land in the raw ring, for the widening ones.  Pages
 // behind the row's end, or that the table does not name, are asked for behind the end of
 // the pool, where a copy delivers zeros.
@@ -474,21 +487,28 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
             if (blk < 0 || blk >= geo.n_blocks) return kMissing;  // a block that the table does not name
             return (int)(((layer + blk) << geo.block_shift) + (j & ((1 << geo.block_shift) - 1)));
         };
-        int slot = kNone, next = slot_of(beg * BN + lane * box);
+        int k_slot = kNone, v_slot = kNone, next = slot_of(beg * BN + lane * box);
         const int total = max(1, 2 * tiles);  // an item without keys still has its queries
         for (int g = 0; g < total; g++) {
             if (g < 2 * tiles) {
                 const int f = fill + g;
-                const bool v = g & 1;
-                if (!v) {  // K and V of a tile come from the same slots; the next tile's are looked up meanwhile
-                    slot = next;
-                    next = g + 2 < 2 * tiles ? slot_of((beg + (g >> 1) + 1) * BN + lane * box) : kNone;
+                const Fill what(g, tiles);
+                const bool v = what.v;
+                // K and V of a tile come from the same slots, which are looked up one tile ahead.
+                int slot;
+                if (!v) {
+                    slot = k_slot = next;
+                    next = what.tile + 1 < tiles ? slot_of((beg + what.tile + 1) * BN + lane * box) : kNone;
+                    if (g == 0) v_slot = k_slot;
+                } else {
+                    slot = v_slot;
+                    v_slot = k_slot;
                 }
                 constexpr int RING = RAW ? C::kRaws : C::kStages;
                 const int st = f % RING, round = f / RING;
                 if (round > 0 && !c.wait(RAW ? c.sh->raw_empty + st : c.sh->empty + st, round - 1)) return;
                 bool mend = false;
-                if (!RAW && v && part.tile<BN>(g >> 1)) {
+                if (!RAW && v && part.tile<BN>(what.tile)) {
                     if (!c.wait(c.sh->scanned + n % kSlots, n / kSlots)) return;
                     mend = b->mend;
                 }
@@ -501,17 +521,36 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
                 __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(bar, RAW ? C::kRawBytes : C::kStageBytes);
                 __syncwarp();
-                if (lane * box < BN) {
-                    const CUtensorMap *map = v ? mv : mk;
-                    const int at = slot < 0 ? pool_end : slot;
-                    if (RAW) {
-                        tma_rows(dst + lane * box * D, map, paged, 0, h, at, bar);
+                const CUtensorMap *map = v ? mv : mk;
+                constexpr int MOST = BN / 8;
+                int at[MOST];
+#pragma unroll
+                for (int i = 0; i < MOST; i++) {
+                    const int from = __shfl_sync(0xffffffffu, slot, i);
+                    at[i] = from < 0 ? pool_end : from;
+                }
+                if (elect_one()) {
+                    if (!paged) {
+                        if (RAW) {
+                            tma2(dst, map, 0, at[0], bar);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < D / 64; x++) tma2(dst + x * C::kSubK, map, 64 * x, at[0], bar);
+                        }
                     } else {
 #pragma unroll
-                        for (int x = 0; x < D / 64; x++)
-                            tma_rows(dst + x * C::kSubK + lane * box * 128, map, paged, 64 * x, h, at, bar);
+                        for (int i = 0; i < MOST; i++) {
+                            if (i * box >= BN) break;
+                            if (RAW) {
+                                tma3(dst + i * box * D, map, 0, h, at[i], bar);
+                            } else {
+#pragma unroll
+                                for (int x = 0; x < D / 64; x++) tma3(dst + x * C::kSubK + i * box * 128, map, 64 * x, h, at[i], bar);
+                            }
+                        }
                     }
                 }
+                __syncwarp();
             }
             if (g == 0 && p.q_tma) {  // the query tiles, behind the first key tile
                 if (n > 0 && !c.wait(&c.sh->q_empty, n - 1)) return;
@@ -569,7 +608,7 @@ __device__ __forceinline__ bool mend(const Ctx<D, SRC> &c, Block *b, int *bad, i
     const Partial part(c.p, *b);
     for (int j = 0; j < tiles; j++) {
         if (!part.tile<BN>(j)) continue;
-        const int f = fill + 2 * j + 1, st = f % C::kStages, key0 = (beg + j) * BN;
+        const int f = fill + v_fill(j, tiles), st = f % C::kStages, key0 = (beg + j) * BN;
         if (!c.wait(c.sh->land + st, *phase >> st)) return false;
         *phase ^= 1u << st;
         unsigned char *at = c.stage(f);
@@ -606,10 +645,11 @@ __device__ __forceinline__ bool widen(const Ctx<D, SRC> &c, Block *b, int *bad, 
     const int tiles = b->tiles(), len = b->len, beg = b->beg;
     const Partial part(c.p, *b);
     for (int g = 0; g < 2 * tiles; g++) {
-        const int f = fill + g, raw = f % RAWS, st = f % C::kStages, key0 = (beg + (g >> 1)) * BN;
+        const Fill what(g, tiles);
+        const int f = fill + g, raw = f % RAWS, st = f % C::kStages, key0 = (beg + what.tile) * BN;
         if (!c.wait(c.sh->raw_full + raw, f / RAWS)) return false;
         if (f >= C::kStages && !c.wait(c.sh->empty + st, f / C::kStages - 1)) return false;
-        const bool check = (g & 1) && part.tile<BN>(g >> 1);
+        const bool check = what.v && part.tile<BN>(what.tile);
         const unsigned char *from = c.sm + C::kSmRaw + raw * C::kRawBytes;
         unsigned char *to = c.stage(f);
         constexpr int BATCH = 8;
@@ -656,10 +696,11 @@ __device__ __forceinline__ bool copy(const Ctx<D, SRC> &c, Block *b, int *bad, i
     const int tiles = b->tiles(), len = b->len, beg = b->beg;
     const Partial part(p, *b);
     const auto hand_over = [&](int g) {  // fill g of the item; its V may need special values taken out first
-        if (ELEM == 2 && (g & 1) && part.tile<BN>(g >> 1))
+        const Fill what(g, tiles);
+        if (ELEM == 2 && what.v && part.tile<BN>(what.tile))
             for (int e = tid; e < ALL; e += C::kLoaders) {
                 uint4 *at = reinterpret_cast<uint4 *>(c.stage(fill + g) + tile_at(e / CH, e % CH, C::kSubK));
-                if (has_special(*at)) *at = take_out<D>(*at, 8 * (e % CH), (beg + (g >> 1)) * BN + e / CH, bad, b);
+                if (has_special(*at)) *at = take_out<D>(*at, 8 * (e % CH), (beg + what.tile) * BN + e / CH, bad, b);
             }
         fence_async_smem();
         mbar_arrive(c.sh->full + (fill + g) % C::kStages);
@@ -668,9 +709,10 @@ __device__ __forceinline__ bool copy(const Ctx<D, SRC> &c, Block *b, int *bad, i
     for (int g = 0; g < 2 * tiles; g++) {
         const int f = fill + g;
         if (f >= C::kStages && !c.wait(c.sh->empty + f % C::kStages, f / C::kStages - 1)) { ok = false; break; }
-        const char *src = g & 1 ? p.V : p.K;
-        const int key0 = (beg + (g >> 1)) * BN;
-        const bool check = (g & 1) && part.tile<BN>(g >> 1);
+        const Fill what(g, tiles);
+        const char *src = what.v ? p.V : p.K;
+        const int key0 = (beg + what.tile) * BN;
+        const bool check = what.v && part.tile<BN>(what.tile);
 #pragma unroll 2
         for (int e = tid; e < ALL; e += C::kLoaders) {
             const int row = e / CH, ch = e % CH, j = key0 + row;
@@ -798,17 +840,18 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
         if (twin) {
             // key tile j for query tile j & 1; the query rows are those of tile 0
             for (int j = 0; j < min(2, tiles); j++) {
-                if (!have(fill + 2 * j)) return;
+                const int fk = fill + k_fill(j);
+                if (!have(fk)) return;
                 if (elect_one()) {
-                    issue_qk<C, D>(q, at(fill + 2 * j), tmem + C::kTmemS(j));
+                    issue_qk<C, D>(q, at(fk), tmem + C::kTmemS(j));
                     mma_commit(c.sh->s_full + j);
-                    release(fill + 2 * j);
+                    release(fk);
                     if (j + 1 == tiles) mma_commit(&c.sh->q_empty);
                 }
                 __syncwarp();
             }
             for (int j = 0; j < tiles; j++) {
-                const int t = j & 1, fv = fill + 2 * j + 1, fk = fv + 3;
+                const int t = j & 1, fv = fill + v_fill(j, tiles), fk = fill + k_fill(j + 2);
                 const int before = t ? done[1] : done[0], used = t ? outs[1] : outs[0];
                 if (!have(fv)) return;
                 if (j < 2 && used > 0 && !c.wait(c.sh->o_free + t, used - 1)) return;
@@ -848,7 +891,7 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
             }
             __syncwarp();
             for (int j = 0; j < tiles; j++) {
-                const int fv = fill + 2 * j + 1, fk = fv + 1;
+                const int fv = fill + v_fill(j, tiles), fk = fill + k_fill(j + 1);
                 bool v = false, k = false;  // V of tile j, K of tile j + 1 have landed
 #pragma unroll 1
                 for (int t = 0; t < 2; t++) {
@@ -895,7 +938,7 @@ __device__ __forceinline__ void issuer(const Ctx<D, SRC> &c) {
             }
             __syncwarp();
             for (int j = 0; j < tiles; j++, at_tile++) {
-                const int fv = fill + 2 * j + 1, fk = fv + 1, sb = at_tile & 1;
+                const int fv = fill + v_fill(j, tiles), fk = fill + k_fill(j + 1), sb = at_tile & 1;
                 if (j + 1 < tiles) {
                     if (!have(fk)) return;
                     if (elect_one()) {
