@@ -70,6 +70,8 @@ def _pd(t):
 
 def _s(stream):
     if stream is None:
+        if torch.cuda.is_initialized():  # the handle itself: a Stream object costs more than some kernels
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -276,17 +278,18 @@ def tri_decode_attention_tc(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torc
            "tri_decode_attention_tc")
 
 
-def _same_device(*ts) -> None:
-    """Kernels are launched on the current device: every tensor has to live there."""
-    cur = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"a tensor on {t.device} in a call on cuda:{cur} (use torch.cuda.device)")
-
-
-def _sized(t, n: int, dtype, what: str) -> None:
-    if t.numel() != n or t.dtype != dtype:
+def _arg(t, dev: int, dtype=None, n: int = -1, what: str = ""):
+    """Address of a contiguous tensor on the current device ``dev``, where kernels are launched (None -> NULL), with
+    its type and number of elements checked where given."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{what or 'a tensor'} on {t.device} in a call on cuda:{dev} (use torch.cuda.device)")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor (call .contiguous())")
+    if (dtype is not None and t.dtype != dtype) or (n >= 0 and t.numel() != n):
         raise ValueError(f"{what}: expected {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
+    return t.data_ptr()
 
 
 def alloc_append_workspace(device=None, stream=None) -> torch.Tensor:
@@ -301,15 +304,16 @@ def tri_append(m: TriModel, kv: TriKvDesc, tokens: TriTokenDesc, key_mode: int, 
     """Rotate new tokens' queries and keys by their positions; write keys, values and positions to the last slots
     of the rows ``kv`` describes.  ``q_out`` bf16 [L][T][Hq][d] (None when the tokens have no q)."""
     q, k = tokens._keep[:2]
-    L, T = m.n_layers, tokens.total_tokens
-    _sized(k, L * T * m.n_kv_heads * m.head_dim, torch.bfloat16, "k")
-    if q is not None:
-        _sized(q, L * T * m.n_q_heads * m.head_dim, torch.bfloat16, "q")
-    if q_out is not None:
-        _sized(q_out, L * T * m.n_q_heads * m.head_dim, torch.bfloat16, "q_out")
-    _same_device(k, q_out, K, V, pos, ws)
-    _check(_L.tri_append(ctypes.byref(m), ctypes.byref(kv), ctypes.byref(tokens), int(key_mode), _p(q_out), _p(K),
-                         _p(V), _p(pos), _p(ws), ws.numel() * ws.element_size(), _s(stream)), "tri_append")
+    dev = torch.cuda.current_device()
+    per = m.n_layers * tokens.total_tokens * m.head_dim
+    if k.numel() != per * m.n_kv_heads or (q is not None and q.numel() != per * m.n_q_heads):
+        raise ValueError("tokens do not match the model's layers, heads and head dim")
+    if k.get_device() != dev:
+        raise ValueError(f"tokens on {k.device} in a call on cuda:{dev} (use torch.cuda.device)")
+    _check(_L.tri_append(ctypes.byref(m), ctypes.byref(kv), ctypes.byref(tokens), int(key_mode),
+                         _arg(q_out, dev, torch.bfloat16, per * m.n_q_heads, "q_out"), _arg(K, dev, what="K"),
+                         _arg(V, dev, what="V"), _arg(pos, dev, torch.int32, what="pos"), _arg(ws, dev, what="ws"),
+                         ws.numel() * ws.element_size(), _s(stream)), "tri_append")
 
 
 def tri_prefill_attention_ws_size(m: TriModel, n_seqs: int, total_tokens: int) -> int:
@@ -331,17 +335,15 @@ def tri_prefill_attention(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.
                           stream=None) -> None:
     """Causal softmax attention of the appended tokens' queries ``q`` bf16 [L][T][Hq][d] over the cache rows that
     end with them -> ``out`` bf16 [L][T][Hq][d], ``lse`` float [L][T][Hq] or None."""
-    rows = m.n_layers * m.n_q_heads * m.head_dim
-    T = q.numel() // rows
-    _sized(q, T * rows, torch.bfloat16, "q")
-    _sized(out, T * rows, torch.bfloat16, "out")
-    _sized(tok_off, kv.n_seqs + 1, torch.int64, "tok_off")
-    if lse is not None:
-        _sized(lse, T * m.n_layers * m.n_q_heads, torch.float32, "lse")
-    _same_device(K, V, q, tok_off, out, lse, ws)
-    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _p(K), _p(V), _p(q), _p(tok_off), T,
-                                    float(softmax_scale), _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size(),
-                                    _s(stream)), "tri_prefill_attention")
+    dev = torch.cuda.current_device()
+    heads, d = m.n_layers * m.n_q_heads, m.head_dim
+    T = q.numel() // (heads * d)
+    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _arg(K, dev, what="K"), _arg(V, dev, what="V"),
+                                    _arg(q, dev, torch.bfloat16, T * heads * d, "q"),
+                                    _arg(tok_off, dev, torch.int64, kv.n_seqs + 1, "tok_off"), T, float(softmax_scale),
+                                    _arg(out, dev, torch.bfloat16, T * heads * d, "out"),
+                                    _arg(lse, dev, torch.float32, T * heads, "lse"), _arg(ws, dev, what="ws"),
+                                    ws.numel() * ws.element_size(), _s(stream)), "tri_prefill_attention")
 
 
 def tri_score_compact(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.Tensor, pos, centres: torch.Tensor,
