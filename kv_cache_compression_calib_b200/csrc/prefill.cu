@@ -24,6 +24,7 @@
 //     at head dim 256) into a ring in shared memory, 128-byte swizzled, one box per 64
 //     dims of a contiguous tile or of a page.  It runs ahead into the next item.
 //   - warp 9: issues every product.
+//     Many small copies take long to issue: for long paged items warp 11 brings V beside it.
 //   - warps 10 and 11: see to V tiles that some row sees in part (below), and widen fp8
 //     tiles to fp16 from a second ring; warp 10 also finds the next item.
 //     Pages of fewer than 8 slots (a swizzle atom) are copied by warps 8, 10 and 11.
@@ -71,6 +72,7 @@ constexpr float kRaise = 8.f;  // log2 of the most a weight may pass 1 before th
 
 // How a cache's tiles come: TMA of bf16, TMA of fp8 and widened, or copied record by record.
 enum { kTma16, kTma8, kCopy16, kCopy8 };
+enum { kBoth, kKeys, kValues };  // what a TMA warp brings
 
 template <int D, int SRC>
 struct Cfg {
@@ -85,7 +87,7 @@ struct Cfg {
     static constexpr int kSubQ = kRows * 128;      // a 64-dim column of a Q tile
     static constexpr int kSubK = BN * 128;         // ... of a K or V tile
     static constexpr bool kF16 = SRC == kTma8 || SRC == kCopy8;  // fp16 operands
-    static constexpr int kLoaders = SRC >= kCopy16 ? 96 : 64;  // threads of the loading warps that fill or mend
+    static constexpr int kLoaders = 96;  // threads that copy
     // tensor memory columns
     static constexpr int kTmemS(int b) { return b * BN; }  // S (and P) of tile b, or buffer b
     static constexpr int kTmemO(int t) { return 256 + t * D; }
@@ -102,7 +104,7 @@ struct Shared {
     alignas(16) uint4 claim;  // cluster launch control's answer
     uint64_t full[STAGES], empty[STAGES], land[STAGES];
     uint64_t raw_full[RAWS + 1], raw_empty[RAWS + 1];
-    uint64_t q_full, q_empty, claimed, drain, twin_done;
+    uint64_t q_full, q_empty, claimed, drain, twin_done, keys_begun;
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];
     uint64_t item_full[kSlots], item_empty[kSlots], scanned[kSlots];
 };
@@ -110,6 +112,7 @@ struct Shared {
 struct Misc {
     uint32_t tmem;
     volatile uint32_t abort_flag;
+    volatile uint32_t land;  // bit st: parity of the next phase of land[st]
 };
 
 // -------------------------------------------------------------------- waits
@@ -381,6 +384,9 @@ struct Ctx {
     Misc *misc;
     uint32_t tmem;
 
+    // Between the loading warps that fill or mend tiles.
+    static constexpr int kHelpers = SRC >= kCopy16 ? 96 : 64;
+    __device__ __forceinline__ void sync_helpers() const { asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory"); }
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t n) const { return role_wait(bar, n & 1u, misc, p.flags); }
     // The n-th item, when it is known; nullptr at the end.
     __device__ __forceinline__ Block *item(int n) const {
@@ -454,12 +460,15 @@ __device__ __forceinline__ bool next_item(const Ctx<D, SRC> &c, int n, int *clai
 
 // -------------------------------------------------------------------- loading
 
-// Warp 8 with TMA.  Where the scan found NaN or infinities, V tiles that are seen in part land on land[stage],
+// An item's copies by TMA: all of them by warp 8, or the queries and K by warp 8 and V by
+// warp 11.
+// Where the scan found NaN or infinities, V tiles that are seen in part land on land[stage],
 // for the mending warps; fp8 tiles land in the raw ring, for the widening ones.  Pages
 // behind the row's end, or that the table does not name, are asked for behind the end of
 // the pool, where a copy delivers zeros.
 template <int D, int SRC>
-__device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap *mk, const CUtensorMap *mv, const CUtensorMap *mq) {
+__device__ __forceinline__ bool tma_item(const Ctx<D, SRC> &c, const CUtensorMap *mk, const CUtensorMap *mv, const CUtensorMap *mq,
+                                         Block *b, int n, int fill, int which) {
     using C = Cfg<D, SRC>;
     constexpr int BN = C::BN;
     constexpr bool RAW = SRC == kTma8;
@@ -470,101 +479,116 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
     const int box = paged ? min(1 << geo.block_shift, BN) : BN;  // slots per copy
     constexpr int kNone = -1, kMissing = -2;
     const int pool_end = (int)(paged ? (int64_t)geo.L * geo.n_blocks << geo.block_shift : geo.total);
-    int fill = 0;
-    for (int n = 0;; n++) {
-        Block *b = c.item(n);
-        if (!b) return;
-        const Partial part(p, *b);
-        const int tiles = b->tiles(), len = b->len, beg = b->beg, h = b->h;
-        const int64_t lo = b->lo, layer = (int64_t)b->l * geo.n_blocks;
-        const int32_t *table = geo.block_table + (int64_t)b->seq * geo.max_blocks;
-        // Slot of the pool that a copy starts at for slot j of the row.
-        const auto slot_of = [&](int j) -> int {
-            if (lane * box >= BN || j >= len) return kNone;
-            if (!paged) return (int)(lo + j);
-            const int bi = j >> geo.block_shift;
-            const int32_t blk = bi < geo.max_blocks ? __ldg(table + bi) : -1;
-            if (blk < 0 || blk >= geo.n_blocks) return kMissing;  // a block that the table does not name
-            return (int)(((layer + blk) << geo.block_shift) + (j & ((1 << geo.block_shift) - 1)));
-        };
-        int k_slot = kNone, v_slot = kNone, next = slot_of(beg * BN + lane * box);
-        const int total = max(1, 2 * tiles);  // an item without keys still has its queries
-        for (int g = 0; g < total; g++) {
-            if (g < 2 * tiles) {
-                const int f = fill + g;
-                const Fill what(g, tiles);
-                const bool v = what.v;
-                // K and V of a tile come from the same slots, which are looked up one tile ahead.
-                int slot;
-                if (!v) {
-                    slot = k_slot = next;
-                    next = what.tile + 1 < tiles ? slot_of((beg + what.tile + 1) * BN + lane * box) : kNone;
-                    if (g == 0) v_slot = k_slot;
-                } else {
-                    slot = v_slot;
-                    v_slot = k_slot;
-                }
-                constexpr int RING = RAW ? C::kRaws : C::kStages;
-                const int st = f % RING, round = f / RING;
-                if (round > 0 && !c.wait(RAW ? c.sh->raw_empty + st : c.sh->empty + st, round - 1)) return;
-                bool mend = false;
-                if (!RAW && v && part.tile<BN>(what.tile)) {
-                    if (!c.wait(c.sh->scanned + n % kSlots, n / kSlots)) return;
-                    mend = b->mend;
-                }
-                uint64_t *bar = RAW ? c.sh->raw_full + st : mend ? c.sh->land + st : c.sh->full + st;
-                const uint32_t dst = smem_u32(RAW ? c.sm + C::kSmRaw + st * C::kRawBytes : c.stage(f));
-                if (slot == kMissing) {
-                    b->any_missing = 1u;
-                    atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(bar, RAW ? C::kRawBytes : C::kStageBytes);
-                __syncwarp();
-                const CUtensorMap *map = v ? mv : mk;
-                constexpr int MOST = BN / 8;
-                int at[MOST];
+    const Partial part(p, *b);
+    const int tiles = b->tiles(), len = b->len, beg = b->beg, h = b->h;
+    const int64_t lo = b->lo, layer = (int64_t)b->l * geo.n_blocks;
+    const int32_t *table = geo.block_table + (int64_t)b->seq * geo.max_blocks;
+    // Slot of the pool that a copy starts at for slot j of the row.
+    const auto slot_of = [&](int j) -> int {
+        if (lane * box >= BN || j >= len) return kNone;
+        if (!paged) return (int)(lo + j);
+        const int bi = j >> geo.block_shift;
+        const int32_t blk = bi < geo.max_blocks ? __ldg(table + bi) : -1;
+        if (blk < 0 || blk >= geo.n_blocks) return kMissing;  // a block that the table does not name
+        return (int)(((layer + blk) << geo.block_shift) + (j & ((1 << geo.block_shift) - 1)));
+    };
+    int k_slot = kNone, v_slot = kNone, next = slot_of(beg * BN + lane * box);
+    const int total = max(1, 2 * tiles);  // an item without keys still has its queries
+    for (int g = 0; g < total; g++) {
+        if (g < 2 * tiles) {
+            const int f = fill + g;
+            const Fill what(g, tiles);
+            const bool v = what.v;
+            // K and V of a tile come from the same slots, which are looked up one tile ahead.
+            const int slot = v ? v_slot : next;
+            if (v) {
+                v_slot = k_slot;
+            } else {
+                k_slot = next;
+                next = what.tile + 1 < tiles ? slot_of((beg + what.tile + 1) * BN + lane * box) : kNone;
+                if (g == 0) v_slot = k_slot;
+            }
+            if (which != kBoth && v != (which == kValues)) continue;
+            constexpr int RING = RAW ? C::kRaws : C::kStages;
+            const int st = f % RING, round = f / RING;
+            if (round > 0 && !c.wait(RAW ? c.sh->raw_empty + st : c.sh->empty + st, round - 1)) return false;
+            bool mend = false;
+            if (!RAW && v && part.tile<BN>(what.tile)) {
+                if (!c.wait(c.sh->scanned + n % kSlots, n / kSlots)) return false;
+                mend = b->mend;
+            }
+            uint64_t *bar = RAW ? c.sh->raw_full + st : mend ? c.sh->land + st : c.sh->full + st;
+            const uint32_t dst = smem_u32(RAW ? c.sm + C::kSmRaw + st * C::kRawBytes : c.stage(f));
+            if (slot == kMissing) {
+                b->any_missing = 1u;
+                atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar, RAW ? C::kRawBytes : C::kStageBytes);
+            __syncwarp();
+            const CUtensorMap *map = v ? mv : mk;
+            constexpr int MOST = BN / 8;
+            int at[MOST];
 #pragma unroll
-                for (int i = 0; i < MOST; i++) {
-                    const int from = __shfl_sync(0xffffffffu, slot, i);
-                    at[i] = from < 0 ? pool_end : from;
-                }
-                if (elect_one()) {
-                    if (!paged) {
-                        if (RAW) {
-                            tma2(dst, map, 0, at[0], bar);
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < D / 64; x++) tma2(dst + x * C::kSubK, map, 64 * x, at[0], bar);
-                        }
+            for (int i = 0; i < MOST; i++) {
+                const int from = __shfl_sync(0xffffffffu, slot, i);
+                at[i] = from < 0 ? pool_end : from;
+            }
+            if (elect_one()) {
+                if (!paged) {
+                    if (RAW) {
+                        tma2(dst, map, 0, at[0], bar);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < MOST; i++) {
-                            if (i * box >= BN) break;
-                            if (RAW) {
-                                tma3(dst + i * box * D, map, 0, h, at[i], bar);
-                            } else {
+                        for (int x = 0; x < D / 64; x++) tma2(dst + x * C::kSubK, map, 64 * x, at[0], bar);
+                    }
+                } else {
 #pragma unroll
-                                for (int x = 0; x < D / 64; x++) tma3(dst + x * C::kSubK + i * box * 128, map, 64 * x, h, at[i], bar);
-                            }
+                    for (int i = 0; i < MOST; i++) {
+                        if (i * box >= BN) break;
+                        if (RAW) {
+                            tma3(dst + i * box * D, map, 0, h, at[i], bar);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < D / 64; x++) tma3(dst + x * C::kSubK + i * box * 128, map, 64 * x, h, at[i], bar);
                         }
                     }
                 }
-                __syncwarp();
             }
-            if (g == 0 && p.q_tma) {  // the query tiles, behind the first key tile
-                if (n > 0 && !c.wait(&c.sh->q_empty, n - 1)) return;
-                const int nt = C::NT == 2 && b->row0 + kRows < b->rows ? 2 : 1;
-                if (lane == 0) mbar_arrive_expect_tx(&c.sh->q_full, (uint32_t)(nt * C::kQBytes));
-                __syncwarp();
-                if (lane < nt * (D / 64)) {
-                    const int t = lane / (D / 64), x = lane % (D / 64);
-                    const int64_t tok = (int64_t)b->l * p.T + b->tok0 + token_of(p, b->row0 + t * kRows);
-                    tma3(smem_u32(c.sm + t * C::kQBytes + x * C::kSubQ), mq, 64 * x, h * geo.G, (int)tok, &c.sh->q_full);
-                }
+            __syncwarp();
+        }
+        if (g == 0 && which == kKeys && lane == 0) mbar_arrive(&c.sh->keys_begun);
+        if (g == 0 && p.q_tma && which != kValues) {  // the query tiles, behind the first key tile
+            if (n > 0 && !c.wait(&c.sh->q_empty, n - 1)) return false;
+            const int nt = C::NT == 2 && b->row0 + kRows < b->rows ? 2 : 1;
+            if (lane == 0) mbar_arrive_expect_tx(&c.sh->q_full, (uint32_t)(nt * C::kQBytes));
+            __syncwarp();
+            if (lane < nt * (D / 64)) {
+                const int t = lane / (D / 64), x = lane % (D / 64);
+                const int64_t tok = (int64_t)b->l * p.T + b->tok0 + token_of(p, b->row0 + t * kRows);
+                tma3(smem_u32(c.sm + t * C::kQBytes + x * C::kSubQ), mq, 64 * x, h * geo.G, (int)tok, &c.sh->q_full);
             }
         }
-        fill += 2 * tiles;
+    }
+    return true;
+}
+
+// Whether an item's V is warp 11's: pages, where warp 10 has time to do the scan alone, that
+// is a long item or one of few rows.  (4 tokens over 27K paged slots 124 -> 106 us, a
+// 512-token chunk over 32K 296 -> 284 us; 2K-token prompts, with every item so, 395 -> 505 us.)
+template <int D, int SRC>
+__device__ __forceinline__ bool two_loaders(const Ctx<D, SRC> &c, const Block &b) {
+    return SRC == kTma16 && c.p.geo.layout == TRI_KV_PAGED && b.tiles() >= (b.twin ? 4 : 64);
+}
+
+// Warp 8 with TMA.
+template <int D, int SRC>
+__device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap *mk, const CUtensorMap *mv, const CUtensorMap *mq) {
+    int fill = 0;
+    for (int n = 0;; n++) {
+        Block *b = c.item(n);
+        if (!b || !tma_item(c, mk, mv, mq, b, n, fill, two_loaders(c, *b) ? kKeys : kBoth)) return;
+        fill += 2 * b->tiles();
         c.leave(n);
     }
 }
@@ -574,7 +598,7 @@ __device__ __forceinline__ void tma_warp(const Ctx<D, SRC> &c, const CUtensorMap
 // NaN or infinite values of V.  Read from global memory: the copies then find them in L2, and
 // shared memory, whose bandwidth the products take, is left alone.
 template <int D, int SRC>
-__device__ __forceinline__ void scan(const Ctx<D, SRC> &c, Block *b) {
+__device__ __forceinline__ void scan(const Ctx<D, SRC> &c, Block *b, int step) {
     constexpr int BN = Cfg<D, SRC>::BN, CH = D / 8, BATCH = 8;
     const Geometry &geo = c.p.geo;
     const int tid = threadIdx.x - 10 * 32;
@@ -585,11 +609,11 @@ __device__ __forceinline__ void scan(const Ctx<D, SRC> &c, Block *b) {
     const int box = paged ? min(1 << geo.block_shift, BN) : BN;
     const int there = paged ? min(stop, (len + box - 1) & -box) : (int)min((int64_t)stop, geo.total - b->lo);
 #pragma unroll 1
-    for (int e0 = start * CH + tid; e0 < there * CH; e0 += 64 * BATCH) {
+    for (int e0 = start * CH + tid; e0 < there * CH; e0 += step * BATCH) {
         uint32_t any = 0;
 #pragma unroll
         for (int k = 0; k < BATCH; k++) {
-            const int e = e0 + 64 * k;
+            const int e = e0 + step * k;
             const int64_t rec = e < there * CH ? record(geo, *b, e / CH) : -1;
             if (rec >= 0) any |= special_bits(*reinterpret_cast<const uint4 *>(c.p.V + (rec * CH + e % CH) * 16));
         }
@@ -600,39 +624,42 @@ __device__ __forceinline__ void scan(const Ctx<D, SRC> &c, Block *b) {
 // Warps 10 and 11 for one item of a bf16 cache: V tiles seen in part get zeros behind
 // the row and their special values taken out, then pass on to full[stage].
 template <int D, int SRC>
-__device__ __forceinline__ bool mend(const Ctx<D, SRC> &c, Block *b, int *bad, int fill, uint32_t *phase) {
+__device__ __forceinline__ bool mend(const Ctx<D, SRC> &c, Block *b, int *bad, int fill, int step) {
     using C = Cfg<D, SRC>;
     constexpr int BN = C::BN, CH = D / 8;
     const int tid = threadIdx.x - 10 * 32;
     const int tiles = b->tiles(), len = b->len, beg = b->beg;
     const Partial part(c.p, *b);
+    uint32_t phase = c.misc->land;  // the last item's warps have left it (sync_helpers)
     for (int j = 0; j < tiles; j++) {
         if (!part.tile<BN>(j)) continue;
         const int f = fill + v_fill(j, tiles), st = f % C::kStages, key0 = (beg + j) * BN;
-        if (!c.wait(c.sh->land + st, *phase >> st)) return false;
-        *phase ^= 1u << st;
+        if (!c.wait(c.sh->land + st, phase >> st)) return false;
+        phase ^= 1u << st;
         unsigned char *at = c.stage(f);
         const auto chunk = [&](int e) { return reinterpret_cast<uint4 *>(at + tile_at(e / CH, e % CH, C::kSubK)); };
         // Only slots that some row does not see, eight chunks of a thread at once; behind the
         // row's end, zeros.
         constexpr int BATCH = 8;
         const int stop = min(BN, len - key0) * CH;
-        for (int e0 = max(0, part.from(j) - key0) * CH + tid; e0 < stop; e0 += 64 * BATCH) {
+        for (int e0 = max(0, part.from(j) - key0) * CH + tid; e0 < stop; e0 += step * BATCH) {
             uint32_t any = 0;
 #pragma unroll
             for (int k = 0; k < BATCH; k++)
-                if (e0 + 64 * k < stop) any |= special_bits(*chunk(e0 + 64 * k));
+                if (e0 + step * k < stop) any |= special_bits(*chunk(e0 + step * k));
             if (any & 0x80008000u) {
 #pragma unroll 1
-                for (int e = e0; e < min(stop, e0 + 64 * BATCH); e += 64)
+                for (int e = e0; e < min(stop, e0 + step * BATCH); e += step)
                     if (has_special(*chunk(e))) *chunk(e) = take_out<D>(*chunk(e), 8 * (e % CH), key0 + e / CH, bad, b);
             }
         }
-        for (int e = stop + tid; e < BN * CH; e += 64) *chunk(e) = make_uint4(0u, 0u, 0u, 0u);
+        for (int e = stop + tid; e < BN * CH; e += step) *chunk(e) = make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
-        asm volatile("bar.sync 1, 64;" ::: "memory");
+        if (step > 32) c.sync_helpers();
+        else __syncwarp();
         if (tid == 0) mbar_arrive(c.sh->full + st);
     }
+    if (tid == 0) c.misc->land = phase;
     return true;
 }
 
@@ -749,10 +776,9 @@ __device__ __forceinline__ bool copy(const Ctx<D, SRC> &c, Block *b, int *bad, i
 
 // Warps 10 and 11 (and 8, where it copies): item after item.
 template <int D, int SRC>
-__device__ __forceinline__ void fill_warps(const Ctx<D, SRC> &c) {
+__device__ __forceinline__ void fill_warps(const Ctx<D, SRC> &c, const CUtensorMap *mk, const CUtensorMap *mv) {
     const int warp = threadIdx.x >> 5;
-    int fill = 0, claims = 0;
-    uint32_t phase = 0;
+    int fill = 0, claims = 0, alones = 0;
     bool more = warp == 10 && next_item(c, 0, &claims);
     for (int n = 0;; n++) {
         // An item is claimed while the one before it runs, not earlier: blocks that are
@@ -766,13 +792,22 @@ __device__ __forceinline__ void fill_warps(const Ctx<D, SRC> &c) {
             if (!c.wait(c.sh->item_empty + (n - 1) % kSlots, (n - 1) / kSlots)) return;
             __syncwarp();
             for (int e = threadIdx.x & 31; e < 3 * D; e += 32) bad[e] = 0x7fffffff;
-            asm volatile("bar.sync 1, %0;" ::"n"(Cfg<D, SRC>::kLoaders) : "memory");
+            c.sync_helpers();
         }
         if constexpr (SRC == kTma16) {
-            scan(c, b);
+            const bool alone = two_loaders(c, *b);  // warp 10 scans and mends alone, warp 11 loads
+            const int step = alone ? 32 : 64;
+            if (!alone || warp == 10) scan(c, b, step);
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(c.sh->scanned + n % kSlots);
-            ok = c.wait(c.sh->scanned + n % kSlots, n / kSlots) && (!b->mend || mend(c, b, bad, fill, &phase));
+            if (alone && warp == 11) {
+                // Not before warp 8 has brought the item's first keys: this warp may be items ahead of
+                // the ring, where the parity of a stage's barrier says nothing.
+                ok = c.wait(&c.sh->keys_begun, alones++) && tma_item(c, mk, mv, mv, b, n, fill, kValues);
+            } else {
+                ok = c.wait(c.sh->scanned + n % kSlots, n / kSlots);
+                if (ok && b->mend) ok = mend(c, b, bad, fill, step);
+            }
             if (ok && more) {
                 if (n > 0) ok = c.wait(c.sh->item_empty + (n - 1) % kSlots, (n - 1) / kSlots);
                 more = ok && next_item(c, n + 1, &claims);
@@ -784,7 +819,7 @@ __device__ __forceinline__ void fill_warps(const Ctx<D, SRC> &c) {
         }
         if (!ok) return;
         fill += 2 * b->tiles();
-        asm volatile("bar.sync 1, %0;" ::"n"(Cfg<D, SRC>::kLoaders) : "memory");  // any_bad is final
+        c.sync_helpers();  // any_bad is final
         c.leave(n);
     }
 }
@@ -1315,6 +1350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.claimed, 1);
         mbar_init(&sh.drain, 1);
+        mbar_init(&sh.keys_begun, 1);
         mbar_init(&sh.twin_done, 4);
         for (int i = 0; i < 2; i++) {
             mbar_init(sh.s_full + i, 1);
@@ -1329,7 +1365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(sh.item_empty + i, 4 * C::NT + 4);  // the softmax warps and warps 8 to 11
         }
         mbar_init_fence();
-        misc.abort_flag = 0u;
+        misc.abort_flag = misc.land = 0u;
     }
     for (int e = threadIdx.x; e < 3 * D; e += kThreads) reinterpret_cast<int *>(sm + C::kSmBad)[e] = 0x7fffffff;
     fence_before();
@@ -1364,7 +1400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 8 && !COPY) {
             tma_warp(c, &mk, &mv, &mq);
         } else {
-            fill_warps(c);
+            fill_warps(c, &mk, &mv);
         }
     }
     __syncwarp();
