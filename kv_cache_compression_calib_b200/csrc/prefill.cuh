@@ -109,7 +109,7 @@ struct Shared {
     alignas(16) uint4 claim;  // cluster launch control's answer
     uint64_t full[STAGES], empty[STAGES], land[STAGES];
     uint64_t raw_full[RAWS + 1], raw_empty[RAWS + 1];
-    uint64_t q_full, q_empty, claimed, drain, twin_done, keys_begun;
+    uint64_t q_full, q_land, q_empty, claimed, drain, twin_done, keys_begun;
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];
     uint64_t item_full[kSlots], item_empty[kSlots], scanned[kSlots];
 };
@@ -572,14 +572,20 @@ __device__ __forceinline__ bool tma_item(const Ctx<D, SRC, FEW> &c, const CUtens
         if (g == 0 && which == kKeys && lane == 0) mbar_arrive(&c.sh->keys_begun);
         if (g == 0 && p.q_tma && which != kValues) {  // the query tiles, behind the first key tile
             if (n > 0 && !c.wait(&c.sh->q_empty, n - 1)) return false;
-            const int nt = C::NT == 2 && b->row0 + kRows < b->rows ? 2 : 1;
-            if (lane == 0) mbar_arrive_expect_tx(&c.sh->q_full, (uint32_t)(nt * C::kQBytes));
+            // (both halves of a twin item scale the same rows where they become fp16)
+            const bool same = C::kF16 && C::kTwins && b->twin;
+            const int nt = same || (C::NT == 2 && b->row0 + kRows < b->rows) ? 2 : 1;
+            uint64_t *bar = C::kF16 ? &c.sh->q_land : &c.sh->q_full;
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(nt * C::kQBytes));
             __syncwarp();
-            if (lane < nt * (D / 64)) {
-                const int t = lane / (D / 64), x = lane % (D / 64);
-                const int64_t tok = (int64_t)b->l * p.T + b->tok0 + token_of(p, b->row0 + t * kRows);
-                tma3(smem_u32(c.sm + t * C::kQBytes + x * C::kSubQ), mq, 64 * x, h * geo.G, (int)tok, &c.sh->q_full);
-            }
+            if (elect_one())
+                for (int t = 0; t < nt; t++) {
+                    const int64_t tok = (int64_t)b->l * p.T + b->tok0 + token_of(p, b->row0 + (same ? 0 : t * kRows));
+#pragma unroll
+                    for (int x = 0; x < D / 64; x++)
+                        tma3(smem_u32(c.sm + t * C::kQBytes + x * C::kSubQ), mq, 64 * x, h * geo.G, (int)tok, bar);
+                }
+            __syncwarp();
         }
     }
     return true;
@@ -1057,15 +1063,18 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC, FEW> &c, const Block &
     float scale = p.scale_log2;
     if (C::kF16) {
         // The thread's own row as fp16, scaled by a power of two: one pass for the largest
-        // magnitude, one to convert.
+        // magnitude, one to convert.  TMA has brought the tile to where the result goes, or the row
+        // is read from global memory.
         constexpr int CH = D / 8, BATCH = 8;
         const uint4 *row = reinterpret_cast<const uint4 *>(p.q + row_of(p, b, min(x, b.rows - 1)) * D);
+        const auto here = [&](int k) { return reinterpret_cast<uint4 *>(c.sm + t * C::kQBytes + tile_at(tid, k, C::kSubQ)); };
+        if (p.q_tma ? !c.wait(&c.sh->q_land, n) : n > 0 && !c.wait(&c.sh->q_empty, n - 1)) return false;
         uint32_t top = 0;
 #pragma unroll 1
         for (int k0 = 0; k0 < CH; k0 += BATCH) {
             uint4 v[BATCH];
 #pragma unroll
-            for (int k = 0; k < BATCH; k++) v[k] = row[k0 + k];
+            for (int k = 0; k < BATCH; k++) v[k] = p.q_tma ? *here(k0 + k) : row[k0 + k];
 #pragma unroll
             for (int k = 0; k < BATCH; k++)
                 top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
@@ -1077,17 +1086,15 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC, FEW> &c, const Block &
         const int up = plain ? 0 : 141 - field;
         const float f1 = __uint_as_float((uint32_t)(127 + up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
         scale = scale / f1 / f2;
-        if (n > 0 && !c.wait(&c.sh->q_empty, n - 1)) return false;
 #pragma unroll 1
         for (int k0 = 0; k0 < CH; k0 += BATCH) {
             uint4 v[BATCH];
 #pragma unroll
-            for (int k = 0; k < BATCH; k++) v[k] = row[k0 + k];
+            for (int k = 0; k < BATCH; k++) v[k] = p.q_tma ? *here(k0 + k) : row[k0 + k];
 #pragma unroll
             for (int k = 0; k < BATCH; k++) {
                 const auto two = [&](uint32_t w) { return f16x2(bf16lo(w) * f1 * f2, bf16hi(w) * f1 * f2); };
-                *reinterpret_cast<uint4 *>(c.sm + t * C::kQBytes + tile_at(tid, k0 + k, C::kSubQ)) =
-                    make_uint4(two(v[k].x), two(v[k].y), two(v[k].z), two(v[k].w));
+                *here(k0 + k) = make_uint4(two(v[k].x), two(v[k].y), two(v[k].z), two(v[k].w));
             }
         }
         fence_async_smem();
@@ -1202,13 +1209,9 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC, FEW> &c, const Block &
             for (int k = 0; k < HALF / 2; k++) {
                 const f32x2 e = fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, off2);
                 float a, d;
-                if (k % 4 == 3) {
-                    ex2_fma(e, a, d);
-                } else {
-                    unpack2(e, a, d);
-                    a = ex2(a);
-                    d = ex2(d);
-                }
+                unpack2(e, a, d);
+                a = ex2(a);
+                d = ex2(d);
                 part_sum[k & 1] = add2(part_sum[k & 1], pack2(a, d));
                 pk[k] = C::kF16 ? f16x2(a, d) : bf16x2(a, d);
             }
@@ -1358,7 +1361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(sh.raw_full + i, 1);
             mbar_init(sh.raw_empty + i, 2);
         }
-        mbar_init(&sh.q_full, p.q_tma ? 1 : 128 * C::NT);
+        mbar_init(&sh.q_full, p.q_tma && !C::kF16 ? 1 : 128 * C::NT);
+        mbar_init(&sh.q_land, 1);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.claimed, 1);
         mbar_init(&sh.drain, 1);
@@ -1536,7 +1540,7 @@ cudaError_t launch_t(PrefillParams p, int64_t units, cudaStream_t s) {
     }
     CUtensorMap mk = {}, mv = {}, mq = {};
     if (SRC < kCopy16 && (!make_map<D, SRC, FEW>(&mk, p.K, p.geo) || !make_map<D, SRC, FEW>(&mv, p.V, p.geo))) return cudaErrorInvalidValue;
-    p.q_tma = C::kTma && kRows % p.geo.G == 0 && p.geo.L * p.T <= 0x7fffffffLL;
+    p.q_tma = SRC < kCopy16 && kRows % p.geo.G == 0 && p.geo.L * p.T <= 0x7fffffffLL;
     if (p.q_tma && !make_q_map<D>(&mq, p)) return cudaErrorInvalidValue;
     cudaError_t e = launch_pdl(kern, dim3((unsigned)(units * p.splits)), dim3(kThreads), smem, s, p, mk, mv, mq);
     if (e != cudaSuccess || p.splits == 1) return e;

@@ -120,28 +120,6 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 }
 __device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
 
-// 2^x of two values on the FMA pipe, which the softmax leaves idle while the
-// special-function unit is its bound.  x = n + f with n the nearest integer (the
-// low bits of x + 1.5 * 2^23) and f in [-1/2, 1/2]; 2^f as 1 + c1 f + .. + c4 f^4,
-// the polynomial of least maximal relative error on that interval (2.8e-6, found
-// by linear programming); n is added to its exponent.  x is held at -127, where the
-// result is exactly 0, and must stay below 128.
-__device__ __forceinline__ void ex2_fma(f32x2 x, float &a, float &b) {
-    float lo, hi;
-    unpack2(x, lo, hi);
-    x = pack2(fmaxf(lo, -127.f), fmaxf(hi, -127.f));
-    const f32x2 r = add2(x, both(12582912.f));
-    const f32x2 f = add2(x, fma2(r, both(-1.f), both(12582912.f)));
-    f32x2 y = fma2(f, both(0.009582853876054287f), both(0.055906426161527634f));
-    y = fma2(y, f, both(0.24024099111557007f));
-    y = fma2(y, f, both(0.6931241750717163f));
-    y = fma2(y, f, both(1.f));
-    float r0, r1, y0, y1;
-    unpack2(r, r0, r1);
-    unpack2(y, y0, y1);
-    a = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23));
-    b = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23));
-}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
