@@ -153,6 +153,7 @@ struct AppendParams {
     int32_t *pos;  // may be null
     unsigned *flags;
     int32_t tile;  // tokens per block step, set at launch
+    unsigned long long div_mul;  // division by the units of a token
     unsigned long long turns[128];  // w_f / 2 pi in 0.64 fixed point
 };
 
