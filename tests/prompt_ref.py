@@ -113,6 +113,34 @@ def attend64(b, scale):
     return out, lse, mag
 
 
+def attend64_rows(b, scale):
+    """attend64 with a row's tokens at once, for larger batches."""
+    G = b.hq // b.h
+    out = torch.full((b.L, b.T, b.hq, b.d), math.nan, dtype=torch.float64, device=b.dev)
+    mag, lse = out.clone(), out[..., 0].clone()
+    K, V = b.K.view(-1, b.d), b.V.view(-1, b.d)
+    rows = lambda t, r: bytes_of(t)[r].view(t.dtype).double()  # noqa: E731
+    for l in range(b.L):
+        for s, n in enumerate(b.new):
+            if n == 0:
+                continue
+            t = slice(int(b.tok[s]), int(b.tok[s]) + n)
+            for x in range(b.h):
+                rec = torch.as_tensor(b.rec((l * b.S + s) * b.h + x)).to(b.dev)
+                N, hs = len(rec), slice(x * G, (x + 1) * G)
+                q = b.q[l, t, hs].double()
+                seen = torch.arange(N, device=b.dev) <= (N - n + torch.arange(n, device=b.dev))[:, None]
+                seen = (seen & (rec >= 0))[:, None]
+                k, v = rows(K, rec.clamp(min=0)), rows(V, rec.clamp(min=0))
+                sc = torch.where(seen, scale * torch.einsum("igd,jd->igj", q, k), -math.inf)
+                lse[l, t, hs] = torch.logsumexp(sc, -1)
+                w = torch.exp(sc - lse[l, t, hs][..., None].clamp(min=-1e300))
+                v = torch.where(seen.any(0).any(0)[:, None], v, 0.0)
+                out[l, t, hs] = torch.einsum("igj,jd->igd", w, v)
+                mag[l, t, hs] = torch.einsum("igj,jd->igd", w, v.abs())
+    return out, lse, mag
+
+
 def score_error(b, scale):
     """Bound of a score's fp32 error: d products summed in fp32, 4 d 2^-24 of scale |q| . |k|
     (at most scale * ||q|| ||k||, the largest of the batch)."""

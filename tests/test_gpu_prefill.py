@@ -37,8 +37,8 @@ def check(b, scale=None, expect=0):
     return out, lse
 
 
-def compare(b, scale, out, lse):
-    ref, rlse, mag = attend64(b, scale)
+def compare(b, scale, out, lse, rule=attend64):
+    ref, rlse, mag = rule(b, scale)
     n = int(b.tok[-1])
     longest = int(np.diff(b.row_off_np).max()) if len(b.row_off_np) > 1 else 0
     eps = score_error(b, scale)
