@@ -1470,16 +1470,16 @@ __global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ Pref
 }
 
 // Items per (layer, KV head): sum over sequences of ceil(n G / R), bounded from what the host knows.
-int64_t most_blocks(int64_t S, int64_t G, int D, int64_t T) {
+inline int64_t most_blocks(int64_t S, int64_t G, int D, int64_t T) {
     const int64_t R = D == 256 ? kRows : 2 * kRows;
-    return T * G / R + std::min(S, T);
+    return (T * G + std::min(S, T) * (R - 1)) / R;
 }
 
 constexpr int kMostParts = 160;  // parts of split rows the workspace holds: one per SM
 
 // Splits of each row over its keys: as many as fill the SMs while a split keeps at least
 // four key tiles of the average row.
-int splits_of(int64_t units, int64_t keys, int D) {
+inline int splits_of(int64_t units, int64_t keys, int D) {
     const int64_t tiles = keys / (D == 256 ? 64 : 128);
     return (int)std::max<int64_t>(
         1, std::min<int64_t>(std::min(sm_count(), kMostParts) / std::max<int64_t>(1, units), tiles / 4));
@@ -1519,7 +1519,7 @@ bool make_q_map(CUtensorMap *m, const PrefillParams &p) {
 }
 
 // TMA wants slot numbers of 31 bits, and pages that fill a swizzle atom of 8 rows.
-bool tma_fits(const Geometry &geo) {
+inline bool tma_fits(const Geometry &geo) {
     const int64_t most = 0x7fffffffLL;
     if (geo.layout == TRI_KV_PAGED) return geo.block_shift >= 3 && geo.n_blocks <= (most / geo.L >> geo.block_shift);
     return geo.total >= 1 && geo.total <= most;
