@@ -172,14 +172,16 @@ __device__ __forceinline__ int64_t row_of(const PrefillParams &p, const Block &b
 }
 
 // The block's share of the work, by one warp: sequence after sequence, each cut into
-// ceil(n G / (128 NT)) blocks, the last rows (most keys) first.
+// ceil(n G / (128 NT)) blocks, the last rows (most keys) first, each for all heads before the
+// next: the shortest items then come last.  (Head after head, every head's long items came
+// behind the short ones of the head before: 8K prompt 523 -> 448 us.)
 template <int D, bool TWINS>
 __device__ __forceinline__ bool find_block(const PrefillParams &p, int idx, int split, Block *out) {
     constexpr int R = kRows * Cfg<D, 0, false>::NT, BN = Cfg<D, 0, false>::BN;
     const Geometry &geo = p.geo;
     const int lane = threadIdx.x & 31;
-    const int lh = idx / p.blocks;
-    int b = idx - lh * p.blocks;
+    int b = idx / (geo.L * geo.H);
+    const int lh = idx - b * (geo.L * geo.H);
     for (int base = 0; base < geo.S; base += 32) {
         const int s = base + lane;
         int64_t t0 = 0, n = 0;
