@@ -414,8 +414,8 @@ tri_status tri_decode_attention_tc(const tri_model *m, const tri_kv_desc *kv, co
  * New tokens of a batch: the rows of the query, key and value projections, packed
  * sequence after sequence.
  *   total_tokens: T >= 0, rows of every token tensor; T may exceed tok_off[n_seqs]
- *                 (a padded batch): rows from tok_off[n_seqs] on are neither read
- *                 nor is anything written for them
+ *                 (a padded batch): what rows from tok_off[n_seqs] on hold does not
+ *                 matter, and nothing is written for them
  *   tok_off:      device int64 [n_seqs + 1], tok_off[0] = 0, non-decreasing,
  *                 tok_off[n_seqs] <= T: sequence s's tokens are rows
  *                 tok_off[s] .. tok_off[s+1]-1, in order
@@ -448,7 +448,8 @@ typedef struct {
  *              given (queries are turned in both)
  *   q_out:     bf16 [n_layers][T][n_q_heads][d], 16-byte aligned, the turned queries
  *              (required with tokens->q, else NULL).  May be tokens->q itself where
- *              q_stride = n_q_heads * d; must not overlap q, k or v otherwise.
+ *              q_stride = n_q_heads * d; must not overlap q, k or v otherwise.  The
+ *              cache must not overlap the tokens or q_out.
  *   K, V, pos: the cache in kv's layout and element type; pos may be NULL.  Only the
  *              new tokens' slots are written.
  *   ws:        at least 256 bytes, 256-byte aligned: only its flag word is used
@@ -480,12 +481,14 @@ tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token
  *              16-byte aligned
  *   tok_off, total_tokens: as in tri_token_desc
  *   softmax_scale: finite, > 0
- *   out:       bf16 [n_layers][T][n_q_heads][d], 16-byte aligned
+ *   out:       bf16 [n_layers][T][n_q_heads][d], 16-byte aligned, not overlapping q
  *   lse:       float [n_layers][T][n_q_heads] or NULL
  *   ws:        tri_prefill_attention_ws_size bytes, 256-byte aligned; first word is
  *              a flag word (TRI_FLAG_ROW_OFFSETS, also for inconsistent tok_off;
- *              TRI_FLAG_BLOCK_TABLE: that key is skipped).  Calls that may run at the
- *              same time need a workspace each.
+ *              TRI_FLAG_BLOCK_TABLE: that key is skipped; TRI_FLAG_STAGE_TIMEOUT: a
+ *              copy or product did not complete within 2 s).  Calls that may run at the
+ *              same time (two captured graphs, say) need a workspace each.
+ * T * G is limited to 2^31 - 256 (TRI_ERR_UNSUPPORTED beyond).
  * Scores, softmax statistics and sums are fp32; the weights e^{s_j - max} enter the
  * product with V as bf16.  Rows of out and lse from tok_off[n_seqs] on are left as
  * they were.

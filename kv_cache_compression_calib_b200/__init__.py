@@ -158,6 +158,8 @@ def tokens(k: torch.Tensor, v: torch.Tensor, tok_off: torch.Tensor, positions: t
         raise ValueError("tokens: q, k, v and positions disagree on the number of tokens, layers or heads")
     if tok_off.dtype != torch.int64 or positions.dtype != torch.int32:
         raise ValueError("tokens: tok_off must be int64 and positions int32")
+    if len({t.device for t in (k, v, tok_off, positions, k if q is None else q)}) != 1:
+        raise ValueError("tokens: tensors on different devices")
     (kp, ks), (vp, vs) = _token_rows(k, "k"), _token_rows(v, "v")
     qp, qs = _token_rows(q, "q") if q is not None else (None, 0)
     d = TriTokenDesc(T, _p(tok_off).value, _p(positions).value, qp, kp, vp, qs, ks, vs)
@@ -292,6 +294,18 @@ def _arg(t, dev: int, dtype=None, n: int = -1, what: str = ""):
     return t.data_ptr()
 
 
+def _cache(kv: TriKvDesc, m: TriModel, t: torch.Tensor, dev: int, what: str):
+    """Address of a cache tensor that holds what ``kv`` describes."""
+    if kv.layout == TRI_KV_PAGED:
+        slots = m.n_layers * kv.n_blocks * kv.block_size * m.n_kv_heads
+    else:
+        slots = kv.total_keys
+    if elem_type_of(t) != kv.elem_type or t.numel() < slots * m.head_dim:
+        raise ValueError(f"{what}: {t.numel()} elements of {t.dtype} do not hold the {slots} records of head dim "
+                         f"{m.head_dim} that the descriptor says")
+    return _arg(t, dev, what=what)
+
+
 def alloc_append_workspace(device=None, stream=None) -> torch.Tensor:
     """The flag word ``tri_append`` reports anomalies in (read with ``tri_status_check``)."""
     ws = torch.empty(256, dtype=torch.uint8, device=device or "cuda")
@@ -311,8 +325,8 @@ def tri_append(m: TriModel, kv: TriKvDesc, tokens: TriTokenDesc, key_mode: int, 
     if k.get_device() != dev:
         raise ValueError(f"tokens on {k.device} in a call on cuda:{dev} (use torch.cuda.device)")
     _check(_L.tri_append(ctypes.byref(m), ctypes.byref(kv), ctypes.byref(tokens), int(key_mode),
-                         _arg(q_out, dev, torch.bfloat16, per * m.n_q_heads, "q_out"), _arg(K, dev, what="K"),
-                         _arg(V, dev, what="V"), _arg(pos, dev, torch.int32, what="pos"), _arg(ws, dev, what="ws"),
+                         _arg(q_out, dev, torch.bfloat16, per * m.n_q_heads, "q_out"), _cache(kv, m, K, dev, "K"),
+                         _cache(kv, m, V, dev, "V"), _arg(pos, dev, torch.int32, what="pos"), _arg(ws, dev, what="ws"),
                          ws.numel() * ws.element_size(), _s(stream)), "tri_append")
 
 
@@ -338,7 +352,7 @@ def tri_prefill_attention(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.
     dev = torch.cuda.current_device()
     heads, d = m.n_layers * m.n_q_heads, m.head_dim
     T = q.numel() // (heads * d)
-    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _arg(K, dev, what="K"), _arg(V, dev, what="V"),
+    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _cache(kv, m, K, dev, "K"), _cache(kv, m, V, dev, "V"),
                                     _arg(q, dev, torch.bfloat16, T * heads * d, "q"),
                                     _arg(tok_off, dev, torch.int64, kv.n_seqs + 1, "tok_off"), T, float(softmax_scale),
                                     _arg(out, dev, torch.bfloat16, T * heads * d, "out"),

@@ -1,5 +1,6 @@
 // extern "C" entry points of libtri.so: argument checks, workspace carving and
 // kernel dispatch.  See include/tri.h for the contract of every call.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -521,7 +522,7 @@ tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token
         (tokens->q == nullptr) != (q_out == nullptr))
         return TRI_ERR_INVALID_ARG;
     if (T > (1LL << 31) - 1 || L * T > (1LL << 40) || m->n_q_heads > (1 << 20)) return TRI_ERR_UNSUPPORTED;
-    const int64_t most = 1LL << 40;  // strides beyond this could pass 64-bit byte offsets
+    const int64_t most = (1LL << 56) / (L * T);  // rows beyond this could pass 64-bit byte offsets
     if (tokens->k_stride < m->n_kv_heads * D || tokens->v_stride < m->n_kv_heads * D || tokens->k_stride > most ||
         tokens->v_stride > most || (tokens->q && (tokens->q_stride < m->n_q_heads * D || tokens->q_stride > most)))
         return TRI_ERR_INVALID_ARG;
@@ -583,12 +584,18 @@ tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, cons
     if (st != TRI_OK) return st;
     Geometry geo;
     if ((st = check_kv(m, kv, &geo)) != TRI_OK) return st;
-    if (total_tokens < 0 || !std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return TRI_ERR_INVALID_ARG;
+    if (total_tokens < 0 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale * 1.4426950408889634f))
+        return TRI_ERR_INVALID_ARG;
     if ((st = check_ws(ws, ws_bytes, tri_prefill_attention_ws_size(m, kv->n_seqs, total_tokens))) != TRI_OK) return st;
     if (total_tokens == 0) return TRI_OK;
     if (!K || !V || !q || !tok_off || !out || out == q) return TRI_ERR_INVALID_ARG;
-    if (total_tokens > (1LL << 31) - 1 || m->n_layers * total_tokens > (1LL << 40) || m->n_q_heads > (1 << 20))
+    // rows of a KV head's product, and items of the grid, are 31-bit numbers
+    if (total_tokens > 0x7fffff00LL / geo.G || m->n_q_heads > (1 << 20) ||
+        (double)(total_tokens * geo.G / 128 + std::min<int64_t>(kv->n_seqs, total_tokens)) * m->n_layers * m->n_kv_heads >
+            (double)(1 << 25))
         return TRI_ERR_UNSUPPORTED;
+    const int64_t bytes = 2 * m->n_layers * total_tokens * m->n_q_heads * m->head_dim;
+    if ((const char *)q < (const char *)out + bytes && (const char *)out < (const char *)q + bytes) return TRI_ERR_INVALID_ARG;
     if (!aligned(K, 16) || !aligned(V, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(tok_off, 8) ||
         (lse && !aligned(lse, 4)))
         return TRI_ERR_ALIGNMENT;

@@ -1554,7 +1554,6 @@ cudaError_t launch_d(const PrefillParams &p0, cudaStream_t s) {
     PrefillParams p = p0;
     const Geometry &geo = p.geo;
     const int64_t blocks = most_blocks(geo.S, geo.G, D, p.T), units = blocks * geo.L * geo.H;
-    p.blocks = (int32_t)blocks;
     int l = 0;
     while ((1 << l) < geo.G) l++;
     p.div_shift = 31 + l;

@@ -169,7 +169,6 @@ struct PrefillParams {
     float *part;        // scratch of split rows
     unsigned *flags;
     // set at launch:
-    int32_t blocks;  // bound of the blocks per (layer, KV head)
     int32_t splits;  // parts each row's keys are cut into
     unsigned long long div_mul;  // division by G
     int32_t div_shift;

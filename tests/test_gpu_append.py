@@ -212,3 +212,20 @@ def test_append_to_a_pool_past_32_bit_offsets():
         blk = int(table[0, j // bs])
         assert torch.equal(K[0, blk, j % bs], k[i]) and torch.equal(V[0, blk, j % bs], v[i]), i
     assert DTYPE["bf16"] == K.dtype and not K[0, 4:nb - 2].any()
+
+
+def test_append_wrong_caches_and_devices_are_refused():
+    b = Batch([3, 2], [1, 0], dev=DEV)
+    q, k, v, pos = make_tokens(b)
+    ws = tri.alloc_append_workspace()
+    t = tri.tokens(k, v, b.tok_off, pos, q=q)
+    out = torch.empty_like(q.contiguous())
+    for K, V, o, P in ((b.K.to(torch.float8_e4m3fn), b.V, out, None), (b.K, b.V[:, 1:].contiguous(), out, None),
+                       (b.K, b.V, out[:, 1:], None), (b.K, b.V, out.float(), None), (b.K, b.V, out, b.pos.long()),
+                       (b.K.cpu(), b.V, out, None), (b.K, b.V.transpose(1, 2), out, None)):
+        with pytest.raises(ValueError):
+            tri.tri_append(b.m, b.kv(), t, tri.TRI_KEYS_POST_ROPE, o, K, V, P, ws)
+    with pytest.raises(ValueError):
+        tri.tokens(k, v, b.tok_off, pos.cpu(), q=q)
+    with pytest.raises(ValueError):
+        tri.tri_append(tri.model(2, b.hq, b.h, 1e4), b.kv(), t, tri.TRI_KEYS_POST_ROPE, out, b.K, b.V, None, ws)

@@ -35,7 +35,7 @@ def prefill(m=M, kv_=None, K=A, V=2 * A, q=3 * A, tok_off=A, T=4, scale=0.1, out
     (dict(v=None), BAD), (dict(q=None), BAD), (dict(q_out=None), BAD), (dict(K=None), BAD), (dict(V=None), BAD),
     (dict(V=80 * A), BAD), (dict(mode=2), BAD), (dict(ws=None), BAD), (dict(ws_bytes=255), SMALL), (dict(ws=A + 64), ALIGN),
     (dict(T=1 << 31), UNSUP), (dict(qs=32 * 128 - 8), BAD), (dict(ks=8 * 128 - 8), BAD), (dict(vs=0), BAD),
-    (dict(ks=-8 * 128), BAD), (dict(qs=1 << 41), BAD), (dict(qs=32 * 128 + 4), ALIGN), (dict(ks=8 * 128 + 2), ALIGN),
+    (dict(ks=-8 * 128), BAD), (dict(qs=1 << 55), BAD), (dict(vs=1 << 62), BAD), (dict(T=1 << 30, ks=1 << 27), BAD), (dict(qs=32 * 128 + 4), ALIGN), (dict(ks=8 * 128 + 2), ALIGN),
     (dict(q=16 * A + 2), ALIGN), (dict(k=32 * A + 8), ALIGN), (dict(q_out=64 * A + 8), ALIGN), (dict(K=80 * A + 8), ALIGN),
     (dict(V=96 * A + 2), ALIGN), (dict(tok_off=A + 4), ALIGN), (dict(positions=A + 2), ALIGN), (dict(pos=A + 1), ALIGN),
     # q_out over the queries (but not exactly in place), over the keys, over the values
@@ -53,7 +53,8 @@ def test_append_refuses(kw, status):
     (dict(scale=float("inf")), BAD), (dict(K=A + 8), ALIGN), (dict(V=A + 8), ALIGN), (dict(q=A + 8), ALIGN), (dict(out=A + 4), ALIGN),
     (dict(tok_off=A + 4), ALIGN), (dict(lse=A + 2), ALIGN), (dict(ws=A + 16), ALIGN), (dict(ws=None), BAD), (dict(ws_bytes=255), SMALL),
     (dict(T=1 << 31), UNSUP), (dict(m=tri.model(1, 32, 8, 1e6, head_dim=32)), UNSUP), (dict(kv_=kv(total=-1)), BAD),
-    (dict(kv_=kv(layout=1)), BAD),
+    (dict(kv_=kv(layout=1)), BAD), (dict(out=3 * A + 4096), BAD), (dict(out=3 * A - 32 * 128 * 8 + 16), BAD), (dict(scale=3e38), BAD),
+    (dict(m=tri.model(1, 128, 1, 1e6), T=1 << 25), UNSUP), (dict(m=tri.model(1 << 20, 8, 8, 1e6), kv_=kv(n_seqs=64), T=64), UNSUP),
 ])
 def test_prefill_refuses(kw, status):
     assert prefill(**kw) == status
