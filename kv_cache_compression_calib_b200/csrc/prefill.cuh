@@ -182,12 +182,17 @@ __device__ __forceinline__ bool find_block(const PrefillParams &p, int idx, int 
     const int lane = threadIdx.x & 31;
     int b = idx / (geo.L * geo.H);
     const int lh = idx - b * (geo.L * geo.H);
+    const int l = lh / geo.H, h = lh - l * geo.H;
     for (int base = 0; base < geo.S; base += 32) {
         const int s = base + lane;
-        int64_t t0 = 0, n = 0;
+        // A lane's sequence: its tokens and, before it is known whose they are, its cache row.
+        int64_t t0 = 0, n = 0, lo = 0, hi = 0;
         if (s < geo.S) {
+            const int64_t r = ((int64_t)l * geo.S + s) * geo.H + h;
             t0 = p.tok_off[s];
             n = p.tok_off[s + 1] - t0;
+            lo = geo.row_off[r];
+            hi = geo.row_off[r + 1];
             if (t0 < 0 || n < 0 || t0 + n > p.T || (s == 0 && t0 != 0)) {
                 atomicOr(p.flags, TRI_FLAG_ROW_OFFSETS);
                 n = 0;
@@ -202,36 +207,40 @@ __device__ __forceinline__ bool find_block(const PrefillParams &p, int idx, int 
         const uint32_t here = __ballot_sync(0xffffffffu, b < upto);
         if (here) {
             if (lane == __ffs(here) - 1) {
-                Block &w = *out;
-                w.l = lh / geo.H;
-                w.h = lh - w.l * geo.H;
-                w.seq = s;
-                w.n = (int)n;
-                w.rows = (int)(n * geo.G);
-                w.row0 = (upto - 1 - b) * R;
-                w.tok0 = t0;
-                const int64_t r = ((int64_t)w.l * geo.S + s) * geo.H + w.h;
-                int64_t lo = geo.row_off[r], hi = geo.row_off[r + 1];
                 if (lo < 0 || hi < lo || hi > geo.total || hi - lo > 0x7fffff00LL) {
                     atomicOr(p.flags, TRI_FLAG_ROW_OFFSETS);
                     hi = lo = 0;
                 }
-                w.lo = lo;
-                w.len = (int)(hi - lo);
+                const int rows = (int)(n * geo.G), row0 = (upto - 1 - b) * R, old = (int)(hi - lo) - (int)n;
                 int c[2] = {0, 0};
+#pragma unroll
                 for (int t = 0; t < Cfg<D, 0, false>::NT; t++) {
-                    const int first = w.row0 + t * kRows;
-                    if (first < w.rows) c[t] = max(0, last_seen(p, w, min(first + kRows, w.rows) - 1) + BN) / BN;
+                    const int first = row0 + t * kRows;
+                    if (first < rows) c[t] = max(0, old + token_of(p, min(first + kRows, rows) - 1) + BN) / BN;
                 }
                 const int all = max(c[0], c[1]);
-                w.beg = p.splits == 1 ? 0 : (int)((int64_t)all * split / p.splits);
+                const int beg = p.splits == 1 ? 0 : (int)((int64_t)all * split / p.splits);
                 const int end = p.splits == 1 ? all : (int)((int64_t)all * (split + 1) / p.splits);
-                for (int t = 0; t < 2; t++) w.cnt[t] = max(0, min(c[t], end) - w.beg);
-                w.twin = TWINS && w.row0 + kRows >= w.rows;
-                if (w.twin) {
-                    w.cnt[1] = w.cnt[0] / 2;
-                    w.cnt[0] -= w.cnt[1];
+                int c0 = max(0, min(c[0], end) - beg), c1 = max(0, min(c[1], end) - beg);
+                const bool twin = TWINS && row0 + kRows >= rows;
+                if (twin) {
+                    c1 = c0 / 2;
+                    c0 -= c1;
                 }
+                Block &w = *out;
+                w.l = l;
+                w.h = h;
+                w.seq = s;
+                w.n = (int)n;
+                w.rows = rows;
+                w.row0 = row0;
+                w.len = (int)(hi - lo);
+                w.tok0 = t0;
+                w.lo = lo;
+                w.beg = beg;
+                w.cnt[0] = c0;
+                w.cnt[1] = c1;
+                w.twin = twin;
             }
             if (idx == 0)  // the first block looks at the offsets of the sequences behind its own, too
                 for (int x = s + 32; x < geo.S; x += 32)
@@ -1352,6 +1361,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&misc.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 8 * 32 && !COPY) {  // the copies' descriptors, before the first needs them
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mk)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mv)) : "memory");
+        if (p.q_tma) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mq)) : "memory");
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; i++) {
