@@ -24,7 +24,7 @@
 //     at head dim 256) into a ring in shared memory, 128-byte swizzled, one box per 64
 //     dims of a contiguous tile or of a page.  It runs ahead into the next item.
 //   - warp 9: issues every product.
-//     Many small copies take long to issue: for long paged items warp 11 brings V beside it.
+//     Many small copies take long to issue: for pages and few rows warp 11 brings V beside it.
 //   - warps 10 and 11: see to V tiles that some row sees in part (below), and widen fp8
 //     tiles to fp16 from a second ring; warp 10 also finds the next item.
 //     Pages of fewer than 8 slots (a swizzle atom) are copied by warps 8, 10 and 11.
@@ -51,6 +51,12 @@
 // warpgroups then take the same rows, one the even key tiles and one the odd ones, and the
 // first merges the two (a "twin" item; one token over a 2K row waits on the chain product -
 // softmax - product, not on memory).
+//
+// Measured (one B200): an 8K prompt of 32/8 heads of 128 448 us, 1.23 PFLOP/s, 62% of
+// the tensor pipe's cycles; a 16K one 1.67 ms, 1.32 PFLOP/s; 4 tokens over 27K slots of 32
+// heads 99 us, 4.5 TB/s.  Per pair of query tiles and 128 keys the loop takes 3140 cycles, 2048 of
+// them the tensor pipe's: each warpgroup's scores, maximum, weights and products are one chain,
+// and the other warpgroup hides two thirds of it.
 //
 // When the items are fewer than the SMs, each row is split over its keys, and
 // prefill_join merges the parts.  Every wait is bounded.
@@ -388,12 +394,6 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x
         : "memory");
 }
 
-// A tile row's box by TMA, x in dims.
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, bool paged, int x, int h, int row, uint64_t *bar) {
-    if (paged) tma3(dst, map, x, h, row, bar);
-    else tma2(dst, map, x, row, bar);
-}
-
 // What the roles of a block share.
 template <int D, int SRC, bool FEW>
 struct Ctx {
@@ -603,8 +603,8 @@ __device__ __forceinline__ bool tma_item(const Ctx<D, SRC, FEW> &c, const CUtens
 }
 
 // Whether an item's V is warp 11's: pages, where warp 10 has time to do the scan alone, that
-// is a long item or one of few rows.  (4 tokens over 27K paged slots 124 -> 106 us, a
-// 512-token chunk over 32K 296 -> 284 us; 2K-token prompts, with every item so, 395 -> 505 us.)
+// is an item of few rows or a long one.  (4 tokens over 27K paged slots 124 -> 106 us;
+// 2K-token prompts, with every item so, 395 -> 505 us.)
 template <int D, int SRC, bool FEW>
 __device__ __forceinline__ bool two_loaders(const Ctx<D, SRC, FEW> &c, const Block &b) {
     return FEW && SRC == kPage16 && b.tiles() >= (b.twin ? 4 : 64);
@@ -1579,9 +1579,8 @@ cudaError_t launch_d(const PrefillParams &p0, cudaStream_t s) {
         return geo.elem_bytes == 1 ? launch_t<D, kCopy8, false>(p, units, s) : launch_t<D, kCopy16, false>(p, units, s);
     // The code for few rows (twin items, keys ahead of values, two loaders) costs whole prompts 5 to
     // 8 percent, by its mere presence in the kernel: it has kernels of its own, for sequences of at most
-    // one query tile on average, and for pages of long rows.
-    const int64_t keys = geo.total / ((int64_t)geo.L * geo.S * geo.H);
-    const bool few = D != 256 && (p.T * geo.G <= kRows * std::min<int64_t>(geo.S, p.T) || (paged && geo.elem_bytes == 2 && keys >= 64 * 128));
+    // one query tile on average.
+    const bool few = D != 256 && p.T * geo.G <= kRows * std::min<int64_t>(geo.S, p.T);
     if (geo.elem_bytes == 1) return few ? launch_t<D, kTma8, D != 256>(p, units, s) : launch_t<D, kTma8, false>(p, units, s);
     if (paged) return few ? launch_t<D, kPage16, D != 256>(p, units, s) : launch_t<D, kPage16, false>(p, units, s);
     return few ? launch_t<D, kTma16, D != 256>(p, units, s) : launch_t<D, kTma16, false>(p, units, s);

@@ -51,9 +51,12 @@ def test_items_of_whole_prompts(layout, elem, d):
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_items_of_long_and_short_pages(d):
-    """Long paged rows, whose values come by a warp of their own, between short ones."""
+    """Long paged rows between short ones; with few tokens, whose values come by a warp of their own, on blocks that
+    take many items."""
     new, old = [300, 40, 700, 3, 280, 1, 200, 17], [20000, 0, 16000, 19000, 30, 21000, 15000, 0]
     check(Batch(new, old, L=2, hq=16, h=8, d=d, dev=DEV, seed=d), times=3)
+    new, old = [70, 3, 150, 1, 1, 2, 90, 1, 1, 5, 1, 64], [9000, 12000, 0, 11000, 8, 700, 9000, 400, 10000, 0, 13000, 600]
+    check(Batch(new * 3, old * 3, L=1, hq=16, h=8, d=d, dev=DEV, seed=d), times=3)
 
 
 @pytest.mark.parametrize("hq,bs", [(24, 16), (40, 16), (16, 4), (24, 2)])
