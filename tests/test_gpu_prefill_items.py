@@ -124,3 +124,28 @@ def test_wrong_device_type_and_size_are_refused():
             tri.tri_prefill_attention(b.m, b.kv(), **{**args, **bad})
     with pytest.raises(tri.TriError):
         tri.tri_prefill_attention(b.m, b.kv(), **{**args, "ws": ws[:256]} if ws.numel() > 256 else {**args, "ws": ws[:128]})
+
+
+@pytest.mark.parametrize("layout", ["paged", "contig"])
+@pytest.mark.parametrize("old", [[5, 3000], [0, 0]])
+def test_no_sequence_has_tokens(layout, old):
+    """A padded batch of nothing: no row is written, nothing is flagged."""
+    b = Batch([0, 0], old, layout=layout, pad=6, dev=DEV)
+    out, lse, ws = call(b, 0.1)
+    assert tri.tri_status_check(ws) == (0, 0)
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    out, _, _ = call(b, 0.1, with_lse=False)
+    assert (out == 7.0).all()
+
+
+def test_workspace_is_reused_by_calls_of_other_shapes():
+    """One workspace, large enough for each, in stream order: split rows, then whole ones, then split ones."""
+    shapes = [Batch([1], [9000], hq=8, h=2, dev=DEV, seed=1), Batch([300, 200], [0, 50], hq=8, h=2, dev=DEV, seed=2),
+              Batch([4, 2], [5000, 7000], hq=8, h=2, d=64, dev=DEV, seed=3)]
+    n = max(tri.tri_prefill_attention_ws_size(b.m, b.S, b.T) for b in shapes)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    tri.tri_workspace_init(ws)
+    got = [call(b, b.d ** -0.5, ws=ws)[:2] for b in shapes + shapes]
+    assert tri.tri_status_check(ws) == (0, 0)
+    for b, (out, lse) in zip(shapes + shapes, got):
+        compare(b, b.d ** -0.5, out, lse, rule=attend64_rows)
