@@ -67,6 +67,7 @@
 #include <cuda_bf16.h>
 
 #include "keys.cuh"
+#include "span.h"
 #include "tc.cuh"
 #include "tensormap.cuh"
 
@@ -632,18 +633,19 @@ __device__ __forceinline__ void scan(const Ctx<D, SRC, FEW> &c, Block *b, int st
     const Geometry &geo = c.p.geo;
     const int tid = threadIdx.x - 10 * 32;
     const Partial part(c.p, *b);
-    const int stop = (b->beg + b->tiles()) * BN, len = b->len;
-    const int start = max(b->beg * BN, min(part.cnt[0] > 0 ? part.first[0] : stop, part.cnt[1] > 0 ? part.first[1] : stop));
+    const int len = b->len;
+    const int seen = min(part.cnt[0] > 0 ? part.first[0] : 0x7fffffff, part.cnt[1] > 0 ? part.first[1] : 0x7fffffff);
     const bool paged = c.paged();
     const int box = paged ? min(1 << geo.block_shift, BN) : BN;
-    const int there = paged ? min(stop, (len + box - 1) & -box) : (int)min((int64_t)stop, geo.total - b->lo);
+    const Span span = unseen_span(b->beg, b->tiles(), BN, seen, paged ? (int64_t)((len + box - 1) & -box) : geo.total - b->lo);
+    const int chunks = span.count * CH;  // counted from the span's start: a row may have 2^31 of them
 #pragma unroll 1
-    for (int e0 = start * CH + tid; e0 < there * CH; e0 += step * BATCH) {
+    for (int e0 = tid; e0 < chunks; e0 += step * BATCH) {
         uint32_t any = 0;
 #pragma unroll
         for (int k = 0; k < BATCH; k++) {
             const int e = e0 + step * k;
-            const int64_t rec = e < there * CH ? record(geo, *b, e / CH) : -1;
+            const int64_t rec = e < chunks ? record(geo, *b, span.start + e / CH) : -1;
             if (rec >= 0) any |= special_bits(*reinterpret_cast<const uint4 *>(c.p.V + (rec * CH + e % CH) * 16));
         }
         if (any & 0x80008000u) b->mend = 1u;
