@@ -294,12 +294,15 @@ def _arg(t, dev: int, dtype=None, n: int = -1, what: str = ""):
     return t.data_ptr()
 
 
-def _cache(kv: TriKvDesc, m: TriModel, t: torch.Tensor, dev: int, what: str):
-    """Address of a cache tensor that holds what ``kv`` describes."""
+def _slots(kv: TriKvDesc, m: TriModel) -> int:
+    """Records (a head's key or value of one slot) of the cache ``kv`` describes."""
     if kv.layout == TRI_KV_PAGED:
-        slots = m.n_layers * kv.n_blocks * kv.block_size * m.n_kv_heads
-    else:
-        slots = kv.total_keys
+        return m.n_layers * kv.n_blocks * kv.block_size * m.n_kv_heads
+    return kv.total_keys
+
+
+def _cache(t: torch.Tensor, slots: int, kv: TriKvDesc, m: TriModel, dev: int, what: str):
+    """Address of a cache tensor that holds the ``slots`` records ``kv`` describes."""
     if elem_type_of(t) != kv.elem_type or t.numel() < slots * m.head_dim:
         raise ValueError(f"{what}: {t.numel()} elements of {t.dtype} do not hold the {slots} records of head dim "
                          f"{m.head_dim} that the descriptor says")
@@ -316,17 +319,23 @@ def alloc_append_workspace(device=None, stream=None) -> torch.Tensor:
 def tri_append(m: TriModel, kv: TriKvDesc, tokens: TriTokenDesc, key_mode: int, q_out, K: torch.Tensor,
                V: torch.Tensor, pos, ws: torch.Tensor, stream=None) -> None:
     """Rotate new tokens' queries and keys by their positions; write keys, values and positions to the last slots
-    of the rows ``kv`` describes.  ``q_out`` bf16 [L][T][Hq][d] (None when the tokens have no q)."""
-    q, k = tokens._keep[:2]
+    of the rows ``kv`` describes.  ``q_out`` bf16 [L][T][Hq][d] (None when the tokens have no q), ``pos`` int32, a
+    position per record of K (or None)."""
+    q, k, _, tok_off, _ = tokens._keep
     dev = torch.cuda.current_device()
     per = m.n_layers * tokens.total_tokens * m.head_dim
     if k.numel() != per * m.n_kv_heads or (q is not None and q.numel() != per * m.n_q_heads):
         raise ValueError("tokens do not match the model's layers, heads and head dim")
+    if tok_off.numel() != kv.n_seqs + 1:
+        raise ValueError(f"tok_off: {tok_off.numel()} offsets for {kv.n_seqs} sequences (expected one more)")
+    slots = _slots(kv, m)
+    if pos is not None and pos.numel() < slots:
+        raise ValueError(f"pos: {pos.numel()} positions for the {slots} records that the descriptor says")
     if k.get_device() != dev:
         raise ValueError(f"tokens on {k.device} in a call on cuda:{dev} (use torch.cuda.device)")
     _check(_L.tri_append(ctypes.byref(m), ctypes.byref(kv), ctypes.byref(tokens), int(key_mode),
-                         _arg(q_out, dev, torch.bfloat16, per * m.n_q_heads, "q_out"), _cache(kv, m, K, dev, "K"),
-                         _cache(kv, m, V, dev, "V"), _arg(pos, dev, torch.int32, what="pos"), _arg(ws, dev, what="ws"),
+                         _arg(q_out, dev, torch.bfloat16, per * m.n_q_heads, "q_out"), _cache(K, slots, kv, m, dev, "K"),
+                         _cache(V, slots, kv, m, dev, "V"), _arg(pos, dev, torch.int32, what="pos"), _arg(ws, dev, what="ws"),
                          ws.numel() * ws.element_size(), _s(stream)), "tri_append")
 
 
@@ -352,7 +361,9 @@ def tri_prefill_attention(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.
     dev = torch.cuda.current_device()
     heads, d = m.n_layers * m.n_q_heads, m.head_dim
     T = q.numel() // (heads * d)
-    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _cache(kv, m, K, dev, "K"), _cache(kv, m, V, dev, "V"),
+    slots = _slots(kv, m)
+    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _cache(K, slots, kv, m, dev, "K"),
+                                    _cache(V, slots, kv, m, dev, "V"),
                                     _arg(q, dev, torch.bfloat16, T * heads * d, "q"),
                                     _arg(tok_off, dev, torch.int64, kv.n_seqs + 1, "tok_off"), T, float(softmax_scale),
                                     _arg(out, dev, torch.bfloat16, T * heads * d, "out"),

@@ -100,3 +100,67 @@ def test_token_rows_of_fused_projections():
         tri._token_rows(x, "x")  # not on a GPU
     with pytest.raises(ValueError):
         tri._token_rows(_Fake(x[0, 0]), "x")
+
+
+class _Device:
+    """Stands in for a CUDA tensor of this many elements (there is no device here)."""
+    is_cuda, device = True, torch.device("cuda:0")
+
+    def __init__(self, dtype, *shape):
+        self.t, self.dtype, self.shape = torch.empty(shape, device="meta"), dtype, torch.Size(shape)
+        self.numel, self.stride, self.dim, self.is_contiguous = self.t.numel, self.t.stride, self.t.dim, self.t.is_contiguous
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return A
+
+
+class _Calls:
+    """Stands in for the library and counts the calls that reach it."""
+
+    def __init__(self):
+        self.n = 0
+
+    def tri_append(self, *a):
+        self.n += 1
+        return 0
+
+
+@pytest.fixture
+def reached(monkeypatch):
+    calls = _Calls()
+    monkeypatch.setattr(tri, "_L", calls)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(tri, "_s", lambda stream: 0)
+    return calls
+
+
+def append_call(layout, S=2, T=5, L=2, h=2, hq=4, d=64, offsets=None, positions=0):
+    """tri_append of T tokens of S sequences into a cache of 100 (contiguous) or 3 * 16 * h * L (paged) records."""
+    i64, i32, bf16 = torch.int64, torch.int32, torch.bfloat16
+    t = tri.tokens(_Device(bf16, L, T, h, d), _Device(bf16, L, T, h, d), _Device(i64, offsets or S + 1), _Device(i32, T))
+    n = 3 * 16 * h * L if layout == "paged" else 100
+    if layout == "paged":
+        kv = tri.kv_paged(S, _Device(i64, L * S * h + 1), 100, _Device(i32, S, 3), 16, 3)
+    else:
+        kv = tri.kv_contig(S, _Device(i64, L * S * h + 1), 100)
+    pos = None if positions is None else _Device(i32, n + positions)
+    tri.tri_append(tri.model(L, hq, h, 1e4, d), kv, t, 0, None, _Device(bf16, n, d), _Device(bf16, n, d), pos,
+                   _Device(torch.uint8, 256))
+
+
+@pytest.mark.parametrize("layout", ["contig", "paged"])
+def test_append_refuses_offsets_and_positions_of_other_sizes(reached, layout):
+    """Fewer token offsets than the kernel reads, or positions than it may write: refused before the library is called."""
+    for good in (dict(), dict(positions=7), dict(positions=None)):
+        append_call(layout, **good)
+    assert reached.n == 3
+    for bad in (dict(offsets=2), dict(offsets=1), dict(offsets=4), dict(positions=-1), dict(positions=-90)):
+        with pytest.raises(ValueError):
+            append_call(layout, **bad)
+    assert reached.n == 3
