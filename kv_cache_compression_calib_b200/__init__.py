@@ -321,7 +321,10 @@ def tri_append(m: TriModel, kv: TriKvDesc, tokens: TriTokenDesc, key_mode: int, 
     """Rotate new tokens' queries and keys by their positions; write keys, values and positions to the last slots
     of the rows ``kv`` describes.  ``q_out`` bf16 [L][T][Hq][d] (None when the tokens have no q), ``pos`` int32, a
     position per record of K (or None)."""
-    q, k, _, tok_off, _ = tokens._keep
+    keep = getattr(tokens, "_keep", None)
+    if keep is None:  # a descriptor filled in by hand holds addresses only: nothing here could check them
+        raise ValueError("tokens: expected what tokens() returns")
+    q, k, _, tok_off, _ = keep
     dev = torch.cuda.current_device()
     per = m.n_layers * tokens.total_tokens * m.head_dim
     if k.numel() != per * m.n_kv_heads or (q is not None and q.numel() != per * m.n_q_heads):

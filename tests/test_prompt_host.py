@@ -164,3 +164,13 @@ def test_append_refuses_offsets_and_positions_of_other_sizes(reached, layout):
         with pytest.raises(ValueError):
             append_call(layout, **bad)
     assert reached.n == 3
+
+
+def test_append_refuses_tokens_made_by_hand(reached):
+    """A descriptor without its tensors, which have to be checked, is refused by name."""
+    kv_, m = tri.kv_contig(2, _Device(torch.int64, 5), 100), tri.model(1, 4, 2, 1e4, 64)
+    made = _abi.TriTokenDesc(5, A, A, None, A, A, 0, 128, 128)
+    with pytest.raises(ValueError, match="tokens"):
+        tri.tri_append(m, kv_, made, 0, None, _Device(torch.bfloat16, 100, 64), _Device(torch.bfloat16, 100, 64), None,
+                       _Device(torch.uint8, 256))
+    assert reached.n == 0
