@@ -489,9 +489,13 @@ tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token
  *              copy or product did not complete within 2 s).  Calls that may run at the
  *              same time (two captured graphs, say) need a workspace each.
  * T * G is limited to 2^31 - 256 (TRI_ERR_UNSUPPORTED beyond).
- * Scores, softmax statistics and sums are fp32; the weights e^{s_j - max} enter the
- * product with V as bf16.  Rows of out and lse from tok_off[n_seqs] on are left as
- * they were.
+ * Scores, softmax statistics and sums are fp32.  The weights enter the product with V
+ * as e^{s_j} over an earlier or the present maximum, rounded to bf16 (off by at most
+ * 2^-8 of themselves).  Over fp8 caches they are fp16 instead (2^-8 of themselves down to
+ * 2^-27 of the row's largest weight, 2^-35 of the largest below that), and so are the
+ * queries, each row scaled by a power of two (elements below 2^-31 of the row's largest
+ * lose bits of their bf16).  Rows of out and lse from tok_off[n_seqs] on are left as they
+ * were.
  */
 size_t tri_prefill_attention_ws_size(const tri_model *m, int32_t n_seqs, int64_t total_tokens);
 tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V, const void *q,

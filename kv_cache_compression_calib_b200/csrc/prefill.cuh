@@ -35,11 +35,13 @@
 // five instructions), exactly.  The queries then have to be fp16 as well: a row is
 // scaled by the power of two that brings its largest value to [2^14, 2^15), which its
 // score scale takes back, so values down to 2^-31 of the largest keep all eight bits of
-// their bf16.  P is fp16, too: weights of at most 2^8 keep eleven bits, and those below
-// 2^-14 an absolute 2^-25.
+// their bf16.  P is fp16, too, whose smallest numbers are not far below 1: the maximum's weight is
+// put to 2^10 and may grow to 2^14, so that weights down to 2^-27 of the largest are as good as
+// in bf16 (half a step, 2^-8), and all within 2^-35 of the largest.  (At 1 and 2^8, keys 17 nats below an
+// attention sink were lost.)
 //
-// The maximum m a row subtracts is only raised when its scores pass it by more than
-// 2^8 (weights up to 256 lose nothing in bf16 or fp32), so O is rescaled rarely.
+// The maximum m a row subtracts is only raised when its weights pass 2^8 (bf16) or 2^14 (fp16),
+// which neither these types nor fp32 mind, so O is rescaled rarely.
 // Statistics and O are fp32; P's rounding to bf16 is the operands' common type.
 //
 // Keys a row must not see get weight exactly 0, but 0 * NaN is NaN in the product:
@@ -77,7 +79,6 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 128;     // rows of a query tile: one per thread of a softmax warpgroup
 constexpr int kSlots = 3;      // items known to the block: the next, the current, the last
-constexpr float kRaise = 8.f;  // log2 of the most a weight may pass 1 before the maximum is raised
 
 // How a cache's tiles come: TMA of bf16 rows or pages, TMA of fp8 and widened, or copied
 // record by record.
@@ -99,6 +100,9 @@ struct Cfg {
     static constexpr bool kTwins = FEW && D != 256;  // items of at most 128 rows are twin items
     static constexpr bool kTma = SRC == kTma16 || SRC == kPage16;  // bf16 by TMA
     static constexpr bool kF16 = SRC == kTma8 || SRC == kCopy8;  // fp16 operands
+    // log2 of a weight of the maximum when it is raised, and of how far weights may pass that before it is
+    // raised again.
+    static constexpr float kLift = kF16 ? 10.f : 0.f, kRaise = kF16 ? 4.f : 8.f;
     static constexpr int kLoaders = 96;  // threads that copy
     // tensor memory columns
     static constexpr int kTmemS(int b) { return b * BN; }  // S (and P) of tile b, or buffer b
@@ -1143,7 +1147,7 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC, FEW> &c, const Block &
     const uint32_t my = c.tmem + ((uint32_t)(tid & ~31) << 16);
     // (The wait for s_full covers every product issued before it: with one query tile, P V of
     // tile j - 2, so of the two o_done barriers none is more than a phase behind its wait.)
-    float m = -INFINITY, sum = 0.f;  // m in units of log2: subtracted from scaled scores
+    float m = -INFINITY, sum = 0.f;  // m in units of log2, kLift below a maximum: subtracted from scaled scores
     for (int j = 0; j < cnt; j++) {
         const int at = before + j;
         const int sb = C::NT == 2 ? t : at & 1;
@@ -1192,9 +1196,9 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC, FEW> &c, const Block &
         }
         float top = max2(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
         if (top == INFINITY) top = NAN;  // inf - inf, as the definition has it
-        // raise the maximum: always from nothing, else once the scores pass it by 2^8
-        if (__any_sync(0xffffffffu, !(top <= m + kRaise))) {
-            const float mn = top <= m + kRaise ? m : top;
+        // raise the maximum: always from nothing, else once the weights pass 2^(kLift + kRaise)
+        if (__any_sync(0xffffffffu, !(top <= m + (C::kLift + C::kRaise)))) {
+            const float mn = top <= m + (C::kLift + C::kRaise) ? m : top - C::kLift;
             if (j > 0) {
                 if (C::NT == 1 && !c.wait(c.sh->o_done + ((at - 1) & 1), (at - 1) >> 1)) return false;
                 fence_after();

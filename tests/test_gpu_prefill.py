@@ -308,3 +308,28 @@ def test_prompt_then_decode():
             assert np.abs(out[0, s, e].double().cpu().numpy() - ref).max() <= 2.0 ** -6.9 * mag
             assert abs(lse[0, s, e].item() - rlse) <= 1e-4 and abs(lse2[0, s, e].item() - rlse) <= 1e-4
     assert math.isfinite(lse.sum().item())
+
+
+@pytest.mark.parametrize("layout,bs", [("contig", 16), ("paged", 16), ("paged", 4)])
+@pytest.mark.parametrize("new,old,h", [(200, 4000, 2), (2, 4000, 64), (1, 3000, 1)])
+@pytest.mark.parametrize("elem", ["fp8", "bf16"])
+def test_prefill_values_behind_a_sink(elem, layout, bs, new, old, h):
+    """One key far above all others, whose value is zero in half the dims: what those dims hold comes from thousands
+    of keys 15.8 to 17.9 nats below it.  Weights 2^-26 of the largest are within half a bf16 step in either type."""
+    b = Batch([new], [old], hq=2 * h, h=h, d=64, elem=elem, layout=layout, bs=bs, dev=DEV, seed=new, v_mean=1.0)
+    K, V = b.rows64(b.K).clone(), b.rows64(b.V).clone()
+    g = torch.Generator().manual_seed(h)
+    # by the first two dims: scores of -1 .. 1, and 16.875 of the sink
+    small = (torch.randint(-16, 17, (K.shape[0],), generator=g).double() / 16 * 4).to(DEV)
+    small = small.to(torch.float8_e4m3fn).double()
+    K[:] = 0
+    K[:, 0] = small
+    for x in range(h):
+        rec = int(b.rec(x)[5])
+        K[rec, 0], K[rec, 1] = 0, 18
+        V[rec, :32] = 0
+    b.K.copy_(K.view(b.K.shape))
+    b.V.copy_(V.view(b.V.shape))
+    b.q.zero_()
+    b.q[..., 0], b.q[..., 1] = 0.25, 0.9375
+    check(b, scale=1.0)
