@@ -483,7 +483,8 @@ tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token
  *   softmax_scale: finite, > 0
  *   out:       bf16 [n_layers][T][n_q_heads][d], 16-byte aligned, not overlapping q
  *   lse:       float [n_layers][T][n_q_heads] or NULL
- *   ws:        tri_prefill_attention_ws_size bytes, 256-byte aligned; first word is
+ *   ws:        tri_prefill_attention_ws_size bytes, 256-byte aligned (a workspace for
+ *              n_seqs and total_tokens serves every call of at most as many); first word is
  *              a flag word (TRI_FLAG_ROW_OFFSETS, also for inconsistent tok_off;
  *              TRI_FLAG_BLOCK_TABLE: that key is skipped; TRI_FLAG_STAGE_TIMEOUT: a
  *              copy or product did not complete within 2 s).  Calls that may run at the

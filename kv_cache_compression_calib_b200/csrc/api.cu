@@ -30,6 +30,8 @@ namespace {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
 int pow2_shift(int32_t x) {
     if (x < 1 || x > 1024 || (x & (x - 1))) return -1;
     int s = 0;
@@ -571,10 +573,8 @@ tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token
 
 size_t tri_prefill_attention_ws_size(const tri_model *m, int32_t n_seqs, int64_t total_tokens) {
     if (check_model(m) != TRI_OK || n_seqs < 1 || total_tokens < 0) return 0;
-    return 256 + ((prefill_scratch_bytes(m->n_layers, n_seqs, m->n_kv_heads, m->n_q_heads / m->n_kv_heads, m->head_dim,
-                                         total_tokens) +
-                   255) &
-                  ~size_t(255));
+    return 256 + align256(prefill_scratch_most(m->n_layers, m->n_kv_heads, m->n_q_heads / m->n_kv_heads, m->head_dim,
+                                               total_tokens));
 }
 
 tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V, const void *q,
@@ -586,7 +586,9 @@ tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, cons
     if ((st = check_kv(m, kv, &geo)) != TRI_OK) return st;
     if (total_tokens < 0 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale * 1.4426950408889634f))
         return TRI_ERR_INVALID_ARG;
-    if ((st = check_ws(ws, ws_bytes, tri_prefill_attention_ws_size(m, kv->n_seqs, total_tokens))) != TRI_OK) return st;
+    // what this call needs, which may be less than tri_prefill_attention_ws_size
+    const size_t scratch = prefill_scratch_bytes(geo.L, geo.S, geo.H, geo.G, geo.D, total_tokens);
+    if ((st = check_ws(ws, ws_bytes, 256 + align256(scratch))) != TRI_OK) return st;
     if (total_tokens == 0) return TRI_OK;
     if (!K || !V || !q || !tok_off || !out || out == q) return TRI_ERR_INVALID_ARG;
     // rows of a KV head's product, and items of the grid, are 31-bit numbers

@@ -192,6 +192,7 @@ cudaError_t launch_attention_tc(const AttnParams &p, int64_t R, cudaStream_t s);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s);
 size_t prefill_scratch_bytes(int64_t L, int64_t S, int64_t H, int64_t G, int D, int64_t T);
+size_t prefill_scratch_most(int64_t L, int64_t H, int64_t G, int D, int64_t T);
 cudaError_t launch_calib_update(const CalibUpdateParams &p, cudaStream_t s);
 cudaError_t launch_stats(const StatsParams &p, cudaStream_t s);
 cudaError_t launch_key_centres(const KeyCentreParams &p, cudaStream_t s);

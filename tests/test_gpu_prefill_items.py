@@ -149,3 +149,19 @@ def test_workspace_is_reused_by_calls_of_other_shapes():
     assert tri.tri_status_check(ws) == (0, 0)
     for b, (out, lse) in zip(shapes + shapes, got):
         compare(b, b.d ** -0.5, out, lse, rule=attend64_rows)
+
+
+def test_workspace_of_the_largest_batch_serves_smaller_ones():
+    """Allocated once for the largest batch (whose rows are not split), then used by calls of fewer tokens (whose
+    rows are): results and flags as with a workspace of their own, and nothing behind its end written."""
+    batches = [Batch([900, 700, 300, 200], [0, 50, 9, 3000], hq=16, h=8, dev=DEV, seed=4),
+               Batch([1], [9000], hq=16, h=8, dev=DEV, seed=5), Batch([5, 1, 3], [5000, 9000, 20], hq=16, h=8, dev=DEV, seed=6)]
+    n = tri.tri_prefill_attention_ws_size(batches[0].m, batches[0].S, batches[0].T)
+    buf = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    ws = buf[:n]
+    tri.tri_workspace_init(ws)
+    for b in batches:
+        out, lse, _ = call(b, 0.1, ws=ws)
+        assert tri.tri_status_check(ws) == (0, 0)
+        compare(b, 0.1, out, lse, rule=attend64_rows)
+    assert (buf[n:] == 0x5A).all()

@@ -174,3 +174,24 @@ def test_append_refuses_tokens_made_by_hand(reached):
         tri.tri_append(m, kv_, made, 0, None, _Device(torch.bfloat16, 100, 64), _Device(torch.bfloat16, 100, 64), None,
                        _Device(torch.uint8, 256))
     assert reached.n == 0
+
+
+@pytest.mark.parametrize("m", [M, tri.model(1, 8, 1, 1e4), tri.model(2, 40, 40, 1e4, 64), tri.model(3, 27, 27, 1e4), tri.model(1, 1, 1, 1e4),
+                               tri.model(1, 64, 2, 1e4, 256), tri.model(64, 64, 8, 1e6), tri.model(1, 300, 1, 1e4)])
+def test_prefill_workspace_serves_smaller_calls(m):
+    """A workspace of n_seqs sequences and total_tokens tokens is enough for every call of at most as many."""
+    sizes = [(s, t) for s in (1, 2, 3, 4, 9, 16, 64) for t in (1, 2, 4, 16, 40, 129, 512, 2000, 8192, 100000)]
+    most = {x: tri.tri_prefill_attention_ws_size(m, *x) for x in sizes}
+    for S, T in sizes:
+        for s, t in sizes:
+            if s <= S and t <= T:
+                assert most[S, T] >= most[s, t]
+                # the size is looked at before the addresses (a missing one here), so no kernel is launched
+                assert prefill(m=m, kv_=kv(n_seqs=s), T=t, K=None, ws_bytes=most[S, T]) == BAD
+
+
+def test_prefill_workspace_of_one_call():
+    """What a call of many tokens needs is its flag word alone, as a workspace made for it alone always was."""
+    assert prefill(kv_=kv(n_seqs=1), T=8192, K=None, ws_bytes=256) == BAD
+    assert prefill(kv_=kv(n_seqs=1), T=1, K=None, ws_bytes=256) == SMALL
+    assert prefill(kv_=kv(n_seqs=1), T=1 << 62, K=None, ws_bytes=256) == BAD
