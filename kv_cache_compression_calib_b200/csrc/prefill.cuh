@@ -1154,7 +1154,8 @@ __device__ __forceinline__ bool softmax(const Ctx<D, SRC, FEW> &c, const Block &
         if (!c.wait(c.sh->s_full + sb, C::NT == 2 ? at : at >> 1)) return false;
         fence_after();
         const int key0 = (beg + j * step) * BN;
-        const bool missing = SRC != kTma16 && b.any_missing;
+        // (the loading warps, tiles ahead, may be setting it: the lanes' readings are made one)
+        const bool missing = SRC != kTma16 && __any_sync(0xffffffffu, b.any_missing);
         if (key0 + BN - 1 > first || missing) {
             // Some row sees the tile only in part, or slots have no block: minus infinity goes to
             // their columns in tensor memory.  (A rolled loop: this code runs once or twice per

@@ -165,3 +165,22 @@ def test_workspace_of_the_largest_batch_serves_smaller_ones():
         assert tri.tri_status_check(ws) == (0, 0)
         compare(b, 0.1, out, lse, rule=attend64_rows)
     assert (buf[n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("elem,bs", [("bf16", 16), ("fp8", 16), ("bf16", 4), ("fp8", 64)])
+@pytest.mark.parametrize("new,old", [([300, 70, 1], [3000, 5000, 9000]), ([2, 1, 3, 1], [6000, 9000, 7000, 300])])
+def test_unnamed_blocks_that_the_copies_meet_tiles_ahead(elem, bs, new, old):
+    """Blocks that the table does not name, in tiles that the copies reach while the softmax is tiles behind: skipped
+    and flagged, the same bits every time."""
+    b = Batch(new, old, hq=8, h=2, d=64, elem=elem, bs=bs, dev=DEV, seed=bs)
+    for s in range(len(new)):
+        there = (new[s] + old[s]) // bs
+        b.table_np[s, [there // 5, there // 2, there // 2 + 1, there - 3]] = [-1, b.nb, -7, b.nb + 9]
+    scale, seen = b.d ** -0.5, None
+    for _ in range(4):
+        out, lse, ws = call(b, scale)
+        assert tri.tri_status_check(ws)[1] == tri.TRI_FLAG_BLOCK_TABLE
+        if seen is None:
+            seen = (out, lse)
+            compare(b, scale, out, lse, rule=attend64_rows)
+        assert torch.equal(out, seen[0]) and torch.equal(lse, seen[1])
