@@ -554,6 +554,20 @@ tri_status tri_score_noalloc(const tri_model *m, const tri_kv_desc *kv, const vo
  */
 tri_status tri_selftest_wait_timeout(void *ws, size_t ws_bytes, uint64_t limit_ns, tri_stream_t stream);
 
+/*
+ * tri_selftest_prefill_timeout - tri_prefill_attention whose waits give up after
+ * wait_tries tries (1 .. 2^26) instead of 2 s; head dims 64 and 256.
+ *
+ * With few tries its blocks give up with copies and products on their way, wait for
+ * those and end, as they would if one never completed: the flag word then has
+ * TRI_FLAG_STAGE_TIMEOUT, rows of out and lse may hold anything, and the context remains
+ * usable.  Returns as tri_prefill_attention does.
+ */
+tri_status tri_selftest_prefill_timeout(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V,
+                                        const void *q, const int64_t *tok_off, int64_t total_tokens,
+                                        float softmax_scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                                        uint32_t wait_tries, tri_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -356,22 +356,33 @@ def alloc_prefill_attention_workspace(m: TriModel, n_seqs: int, total_tokens: in
     return ws
 
 
+def _prefill_args(m, kv, K, V, q, tok_off, softmax_scale, out, lse, ws):
+    dev = torch.cuda.current_device()
+    heads, d = m.n_layers * m.n_q_heads, m.head_dim
+    T = q.numel() // (heads * d)
+    slots = _slots(kv, m)
+    return (ctypes.byref(m), ctypes.byref(kv), _cache(K, slots, kv, m, dev, "K"), _cache(V, slots, kv, m, dev, "V"),
+            _arg(q, dev, torch.bfloat16, T * heads * d, "q"), _arg(tok_off, dev, torch.int64, kv.n_seqs + 1, "tok_off"), T,
+            float(softmax_scale), _arg(out, dev, torch.bfloat16, T * heads * d, "out"),
+            _arg(lse, dev, torch.float32, T * heads, "lse"), _arg(ws, dev, what="ws"), ws.numel() * ws.element_size())
+
+
 def tri_prefill_attention(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.Tensor, q: torch.Tensor,
                           tok_off: torch.Tensor, softmax_scale: float, out: torch.Tensor, lse, ws: torch.Tensor,
                           stream=None) -> None:
     """Causal softmax attention of the appended tokens' queries ``q`` bf16 [L][T][Hq][d] over the cache rows that
     end with them -> ``out`` bf16 [L][T][Hq][d], ``lse`` float [L][T][Hq] or None."""
-    dev = torch.cuda.current_device()
-    heads, d = m.n_layers * m.n_q_heads, m.head_dim
-    T = q.numel() // (heads * d)
-    slots = _slots(kv, m)
-    _check(_L.tri_prefill_attention(ctypes.byref(m), ctypes.byref(kv), _cache(K, slots, kv, m, dev, "K"),
-                                    _cache(V, slots, kv, m, dev, "V"),
-                                    _arg(q, dev, torch.bfloat16, T * heads * d, "q"),
-                                    _arg(tok_off, dev, torch.int64, kv.n_seqs + 1, "tok_off"), T, float(softmax_scale),
-                                    _arg(out, dev, torch.bfloat16, T * heads * d, "out"),
-                                    _arg(lse, dev, torch.float32, T * heads, "lse"), _arg(ws, dev, what="ws"),
-                                    ws.numel() * ws.element_size(), _s(stream)), "tri_prefill_attention")
+    _check(_L.tri_prefill_attention(*_prefill_args(m, kv, K, V, q, tok_off, softmax_scale, out, lse, ws), _s(stream)),
+           "tri_prefill_attention")
+
+
+def tri_selftest_prefill_timeout(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.Tensor, q: torch.Tensor,
+                                 tok_off: torch.Tensor, softmax_scale: float, out: torch.Tensor, lse, ws: torch.Tensor,
+                                 wait_tries: int, stream=None) -> None:
+    """``tri_prefill_attention`` (head dims 64 and 256) whose waits give up after ``wait_tries`` tries: with few, its
+    blocks end early and set TRI_FLAG_STAGE_TIMEOUT (read it with ``tri_status_check``)."""
+    _check(_L.tri_selftest_prefill_timeout(*_prefill_args(m, kv, K, V, q, tok_off, softmax_scale, out, lse, ws),
+                                           int(wait_tries), _s(stream)), "tri_selftest_prefill_timeout")
 
 
 def tri_score_compact(m: TriModel, kv: TriKvDesc, K: torch.Tensor, V: torch.Tensor, pos, centres: torch.Tensor,

@@ -577,9 +577,10 @@ size_t tri_prefill_attention_ws_size(const tri_model *m, int32_t n_seqs, int64_t
                                                total_tokens));
 }
 
-tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V, const void *q,
-                                 const int64_t *tok_off, int64_t total_tokens, float softmax_scale, void *out,
-                                 float *lse, void *ws, size_t ws_bytes, tri_stream_t stream) {
+// wait_tries > 0: the self-test's kernels, whose waits give up after so many tries.
+static tri_status prefill_attention(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V, const void *q,
+                                    const int64_t *tok_off, int64_t total_tokens, float softmax_scale, void *out, float *lse,
+                                    void *ws, size_t ws_bytes, uint32_t wait_tries, tri_stream_t stream) {
     tri_status st = check_model(m);
     if (st != TRI_OK) return st;
     Geometry geo;
@@ -614,7 +615,24 @@ tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, cons
     p.lse = lse;
     p.part = (float *)((char *)ws + 256);
     p.flags = (unsigned *)((char *)ws + kWsFlags);
-    return cuda_status(launch_prefill(p, (cudaStream_t)stream), "prefill attention kernel launch");
+    p.wait_tries = wait_tries;
+    return cuda_status(wait_tries > 0 ? launch_prefill_selftest(p, (cudaStream_t)stream) : launch_prefill(p, (cudaStream_t)stream),
+                       "prefill attention kernel launch");
+}
+
+tri_status tri_prefill_attention(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V, const void *q,
+                                 const int64_t *tok_off, int64_t total_tokens, float softmax_scale, void *out,
+                                 float *lse, void *ws, size_t ws_bytes, tri_stream_t stream) {
+    return prefill_attention(m, kv, K, V, q, tok_off, total_tokens, softmax_scale, out, lse, ws, ws_bytes, 0, stream);
+}
+
+tri_status tri_selftest_prefill_timeout(const tri_model *m, const tri_kv_desc *kv, const void *K, const void *V,
+                                        const void *q, const int64_t *tok_off, int64_t total_tokens, float softmax_scale,
+                                        void *out, float *lse, void *ws, size_t ws_bytes, uint32_t wait_tries,
+                                        tri_stream_t stream) {
+    if (wait_tries < 1 || wait_tries > (1u << 26)) return TRI_ERR_INVALID_ARG;
+    if (m && m->head_dim == 128) return TRI_ERR_UNSUPPORTED;
+    return prefill_attention(m, kv, K, V, q, tok_off, total_tokens, softmax_scale, out, lse, ws, ws_bytes, wait_tries, stream);
 }
 
 tri_status tri_status_check(void *ws, uint32_t *flags, tri_stream_t stream) {

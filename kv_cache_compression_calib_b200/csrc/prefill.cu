@@ -6,6 +6,8 @@ namespace tri {
 cudaError_t launch_prefill_d64(const PrefillParams &p, cudaStream_t s);
 cudaError_t launch_prefill_d128(const PrefillParams &p, cudaStream_t s);
 cudaError_t launch_prefill_d256(const PrefillParams &p, cudaStream_t s);
+cudaError_t launch_prefill_selftest_d64(const PrefillParams &p, cudaStream_t s);
+cudaError_t launch_prefill_selftest_d256(const PrefillParams &p, cudaStream_t s);
 
 namespace {
 size_t part_bytes(int D) { return (size_t)(D == 256 ? kRows : 2 * kRows) * (D + 2) * sizeof(float); }
@@ -29,6 +31,14 @@ cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s) {
         case 64: return launch_prefill_d64(p, s);
         case 128: return launch_prefill_d128(p, s);
         case 256: return launch_prefill_d256(p, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prefill_selftest(const PrefillParams &p, cudaStream_t s) {
+    switch (p.geo.D) {
+        case 64: return launch_prefill_selftest_d64(p, s);
+        case 256: return launch_prefill_selftest_d256(p, s);
     }
     return cudaErrorInvalidValue;
 }

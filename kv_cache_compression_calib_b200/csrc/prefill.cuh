@@ -61,7 +61,11 @@
 // and the other warpgroup hides two thirds of it.
 //
 // When the items are fewer than the SMs, each row is split over its keys, and
-// prefill_join merges the parts.  Every wait is bounded.
+// prefill_join merges the parts.
+//
+// Every wait is bounded.  A warp whose wait runs out sets the flag and the block's mark, on which the
+// others give up in their next long wait; when all have, the block waits (bounded again) for copies and
+// products on their way and gives its tensor memory back.
 #pragma once
 
 #include <algorithm>
@@ -72,6 +76,14 @@
 #include "span.h"
 #include "tc.cuh"
 #include "tensormap.cuh"
+
+// How a wait tries, when it looks whether its time is over (a try lasts up to some 16 us), and whether
+// it gives up before that: the self-test of the waits has them end after a given number of short tries.
+#ifndef TRI_WAIT_TRY
+#define TRI_WAIT_TRY mbar_test
+#define TRI_WAIT_LOOK(it, p) (((it) & 4095u) == 0)
+#define TRI_WAIT_OVER(it, p) false
+#endif
 
 namespace tri {
 namespace {
@@ -84,6 +96,7 @@ constexpr int kSlots = 3;      // items known to the block: the next, the curren
 // record by record.
 enum { kTma16, kPage16, kTma8, kCopy16, kCopy8 };
 enum { kBoth, kKeys, kValues };  // what a TMA warp brings
+constexpr uint32_t kMends = 0x80000000u, kOdd = 0x40000000u;  // marks of a copy in flight
 
 template <int D, int SRC, bool FEW>
 struct Cfg {
@@ -122,7 +135,10 @@ struct Shared {
     uint64_t raw_full[RAWS + 1], raw_empty[RAWS + 1];
     uint64_t q_full, q_land, q_empty, claimed, drain, twin_done, keys_begun;
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];
-    uint64_t item_full[kSlots], item_empty[kSlots], scanned[kSlots];
+    uint64_t item_full[kSlots], item_empty[kSlots], scanned[kSlots], helpers;
+    // Per stage of the ring that copies land in, its last fill, and for the queries their item; with kMends
+    // where the fill is mended, kOdd beside it where its phase of land is odd; -1 for none.
+    uint32_t in_flight[STAGES + 1];
 };
 
 struct Misc {
@@ -133,20 +149,25 @@ struct Misc {
 
 // -------------------------------------------------------------------- waits
 
-// Bounded wait of one role (the clock is read once in 4096 tries).  When it runs out
-// the block is told to stop.
-__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Misc *misc, unsigned *flags) {
+// Bounded wait of one role's warp (the clock is read once in 4096 tries).  When it runs out
+// the block is told to stop.  The warp gives up only where all its lanes still wait: a lane
+// that saw the barrier complete just as others gave up would wait for them in the collective
+// instructions that follow.  (A vote on every wait instead: 7% on prompts.)
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Misc *misc, const PrefillParams &p) {
     unsigned long long t0 = 0;
-    for (uint32_t it = 1; it < kStageWaitIters; it++) {
-        if (mbar_test(bar, parity)) return true;
-        if ((it & 4095u) == 0) {
+    for (uint32_t it = 1;; it++) {
+        if (TRI_WAIT_TRY(bar, parity)) return true;
+        if (TRI_WAIT_LOOK(it, p)) {
             const unsigned long long t = global_ns();
             if (t0 == 0) t0 = t;
-            if (t - t0 > kStageWaitNs || misc->abort_flag) break;
+            if (__activemask() == 0xffffffffu &&
+                __any_sync(0xffffffffu, TRI_WAIT_OVER(it, p) || t - t0 > kStageWaitNs || misc->abort_flag))
+                break;
+            if (it >= kStageWaitIters) break;
         }
     }
     misc->abort_flag = 1u;
-    atomicOr(flags, TRI_FLAG_STAGE_TIMEOUT);
+    atomicOr(p.flags, TRI_FLAG_STAGE_TIMEOUT);
     return false;
 }
 
@@ -416,8 +437,13 @@ struct Ctx {
     __device__ __forceinline__ bool paged() const {
         return SRC == kTma16 ? false : SRC == kPage16 ? true : p.geo.layout == TRI_KV_PAGED;
     }
-    __device__ __forceinline__ void sync_helpers() const { asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory"); }
-    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t n) const { return role_wait(bar, n & 1u, misc, p.flags); }
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t n) const { return role_wait(bar, n & 1u, misc, p); }
+    // A barrier of the helpers that gives up as every wait does; `syncs` counts a warp's.
+    __device__ __forceinline__ bool sync_helpers(int *syncs) const {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->helpers);
+        return wait(&sh->helpers, (*syncs)++);
+    }
     // The n-th item, when it is known; nullptr at the end.
     __device__ __forceinline__ Block *item(int n) const {
         if (!wait(sh->item_full + n % kSlots, n / kSlots)) return nullptr;
@@ -431,6 +457,16 @@ struct Ctx {
     }
     // Per dim, the first slot whose V is NaN, +inf, -inf there (any_bad of the item says whether any is).
     __device__ __forceinline__ int *bad() const { return reinterpret_cast<int *>(sm + C::kSmBad); }
+    // One warp, when no more copies are asked for: those on their way have landed.
+    __device__ __forceinline__ void drain_copies() const {
+        const int st = threadIdx.x & 31;
+        constexpr int RING = SRC == kTma8 ? C::kRaws : C::kStages;
+        if (st > C::kStages || sh->in_flight[st] == 0xffffffffu) return;
+        const uint32_t mark = sh->in_flight[st];
+        if (st == C::kStages) mbar_wait(C::kF16 ? &sh->q_land : &sh->q_full, mark & 1);
+        else if (mark & kMends) mbar_wait(sh->land + st, mark & kOdd ? 1u : 0u);
+        else mbar_wait(SRC == kTma8 ? sh->raw_full + st : sh->full + st, (mark / RING) & 1);
+    }
     __device__ __forceinline__ unsigned char *stage(int f) const { return sm + C::kSmRing + (f % C::kStages) * C::kStageBytes; }
 };
 
@@ -449,7 +485,11 @@ __device__ __forceinline__ int claim_block(const Ctx<D, SRC, FEW> &c, int *claim
             : "memory");
     }
     __syncwarp();
-    if (!c.wait(&c.sh->claimed, (*claims)++)) return -1;
+    if (!c.wait(&c.sh->claimed, *claims)) {
+        mbar_wait(&c.sh->claimed, *claims & 1);  // the answer is on its way into this block's memory
+        return -1;
+    }
+    ++*claims;
     uint32_t got, x;
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\tld.shared.b128 r, [%2];\n\t"
@@ -541,9 +581,11 @@ __device__ __forceinline__ bool tma_item(const Ctx<D, SRC, FEW> &c, const CUtens
             const int st = f % RING, round = f / RING;
             if (round > 0 && !c.wait(RAW ? c.sh->raw_empty + st : c.sh->empty + st, round - 1)) return false;
             bool mend = false;
+            uint32_t mark = (uint32_t)f;
             if (!RAW && v && part.tile<BN>(what.tile)) {
                 if (!c.wait(c.sh->scanned + n % kSlots, n / kSlots)) return false;
                 mend = b->mend;
+                if (mend) mark = kMends | (mbar_test_now(c.sh->land + st, 0) ? kOdd : 0u);
             }
             uint64_t *bar = RAW ? c.sh->raw_full + st : mend ? c.sh->land + st : c.sh->full + st;
             const uint32_t dst = smem_u32(RAW ? c.sm + C::kSmRaw + st * C::kRawBytes : c.stage(f));
@@ -552,7 +594,10 @@ __device__ __forceinline__ bool tma_item(const Ctx<D, SRC, FEW> &c, const CUtens
                 atomicOr(p.flags, TRI_FLAG_BLOCK_TABLE);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar, RAW ? C::kRawBytes : C::kStageBytes);
+            if (lane == 0) {
+                c.sh->in_flight[st] = mark;
+                mbar_arrive_expect_tx(bar, RAW ? C::kRawBytes : C::kStageBytes);
+            }
             __syncwarp();
             const CUtensorMap *map = v ? mv : mk;
             constexpr int MOST = BN / 8;
@@ -592,7 +637,10 @@ __device__ __forceinline__ bool tma_item(const Ctx<D, SRC, FEW> &c, const CUtens
             const bool same = C::kF16 && C::kTwins && b->twin;
             const int nt = same || (C::NT == 2 && b->row0 + kRows < b->rows) ? 2 : 1;
             uint64_t *bar = C::kF16 ? &c.sh->q_land : &c.sh->q_full;
-            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(nt * C::kQBytes));
+            if (lane == 0) {
+                c.sh->in_flight[C::kStages] = (uint32_t)n;
+                mbar_arrive_expect_tx(bar, (uint32_t)(nt * C::kQBytes));
+            }
             __syncwarp();
             if (elect_one())
                 for (int t = 0; t < nt; t++) {
@@ -659,7 +707,7 @@ __device__ __forceinline__ void scan(const Ctx<D, SRC, FEW> &c, Block *b, int st
 // Warps 10 and 11 for one item of a bf16 cache: V tiles seen in part get zeros behind
 // the row and their special values taken out, then pass on to full[stage].
 template <int D, int SRC, bool FEW>
-__device__ __forceinline__ bool mend(const Ctx<D, SRC, FEW> &c, Block *b, int *bad, int fill, int step) {
+__device__ __forceinline__ bool mend(const Ctx<D, SRC, FEW> &c, Block *b, int *bad, int fill, int step, int *syncs) {
     using C = Cfg<D, SRC, FEW>;
     constexpr int BN = C::BN, CH = D / 8;
     const int tid = threadIdx.x - 10 * 32;
@@ -690,8 +738,8 @@ __device__ __forceinline__ bool mend(const Ctx<D, SRC, FEW> &c, Block *b, int *b
         }
         for (int e = stop + tid; e < BN * CH; e += step) *chunk(e) = make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
-        if (step > 32) c.sync_helpers();
-        else __syncwarp();
+        __syncwarp();
+        if (step > 32 && !c.sync_helpers(syncs)) return false;
         if (tid == 0) mbar_arrive(c.sh->full + st);
     }
     if (tid == 0) c.misc->land = phase;
@@ -813,7 +861,7 @@ __device__ __forceinline__ bool copy(const Ctx<D, SRC, FEW> &c, Block *b, int *b
 template <int D, int SRC, bool FEW>
 __device__ __forceinline__ void fill_warps(const Ctx<D, SRC, FEW> &c, const CUtensorMap *mk, const CUtensorMap *mv) {
     const int warp = threadIdx.x >> 5;
-    int fill = 0, claims = 0, alones = 0;
+    int fill = 0, claims = 0, alones = 0, syncs = 0;
     bool more = warp == 10 && next_item(c, 0, &claims);
     for (int n = 0;; n++) {
         // An item is claimed while the one before it runs, not earlier: blocks that are
@@ -827,7 +875,7 @@ __device__ __forceinline__ void fill_warps(const Ctx<D, SRC, FEW> &c, const CUte
             if (!c.wait(c.sh->item_empty + (n - 1) % kSlots, (n - 1) / kSlots)) return;
             __syncwarp();
             for (int e = threadIdx.x & 31; e < 3 * D; e += 32) bad[e] = 0x7fffffff;
-            c.sync_helpers();
+            if (!c.sync_helpers(&syncs)) return;
         }
         if constexpr (Cfg<D, SRC, FEW>::kTma) {
             const bool alone = two_loaders(c, *b);  // warp 10 scans and mends alone, warp 11 loads
@@ -841,7 +889,7 @@ __device__ __forceinline__ void fill_warps(const Ctx<D, SRC, FEW> &c, const CUte
                 ok = c.wait(&c.sh->keys_begun, alones++) && tma_item(c, mk, mv, mv, b, n, fill, kValues);
             } else {
                 ok = c.wait(c.sh->scanned + n % kSlots, n / kSlots);
-                if (ok && b->mend) ok = mend(c, b, bad, fill, step);
+                if (ok && b->mend) ok = mend(c, b, bad, fill, step, &syncs);
             }
             if (ok && more) {
                 if (n > 0) ok = c.wait(c.sh->item_empty + (n - 1) % kSlots, (n - 1) / kSlots);
@@ -854,7 +902,7 @@ __device__ __forceinline__ void fill_warps(const Ctx<D, SRC, FEW> &c, const CUte
         }
         if (!ok) return;
         fill += 2 * b->tiles();
-        c.sync_helpers();  // any_bad is final
+        if (!c.sync_helpers(&syncs)) return;  // any_bad is final
         c.leave(n);
     }
 }
@@ -1380,6 +1428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(sh.empty + i, 1);
             mbar_init(sh.land + i, 1);
         }
+        for (int i = 0; i <= C::kStages; i++) sh.in_flight[i] = 0xffffffffu;
         for (int i = 0; i <= C::kRaws; i++) {
             mbar_init(sh.raw_full + i, 1);
             mbar_init(sh.raw_empty + i, 2);
@@ -1391,6 +1440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.drain, 1);
         mbar_init(&sh.keys_begun, 1);
         mbar_init(&sh.twin_done, 4);
+        mbar_init(&sh.helpers, Ctx<D, SRC, FEW>::kHelpers / 32);
         for (int i = 0; i < 2; i++) {
             mbar_init(sh.s_full + i, 1);
             mbar_init(sh.p_half + i, 4);
@@ -1431,11 +1481,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_down<88>();
         if (warp == 9) {
             issuer(c);
-            __syncwarp();
-            if (misc.abort_flag && elect_one()) {  // after a wait ran out: products in flight end before their memory is released
-                mma_commit(&sh.drain);
-                mbar_wait(&sh.drain, 0);
-            }
         } else if (warp == 8 && !COPY) {
             tma_warp(c, &mk, &mv, &mq);
         } else {
@@ -1445,6 +1490,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     fence_before();
     __syncthreads();
+    if (misc.abort_flag) {  // after a wait ran out: what is still on its way ends before its memory is released
+        if (warp == 9 && elect_one()) {
+            mma_commit(&sh.drain);
+            mbar_wait(&sh.drain, 0);
+        }
+        if (warp == 8) c.drain_copies();
+        __syncwarp();
+        __syncthreads();
+    }
     fence_after();
     if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(misc.tmem) : "memory");
     grid_dependents_launch();

@@ -168,6 +168,7 @@ struct PrefillParams {
     float *lse;         // [L][T][Hq] or null
     float *part;        // scratch of split rows
     unsigned *flags;
+    uint32_t wait_tries;  // self-test: tries after which a wait gives up
     // set at launch:
     int32_t splits;  // parts each row's keys are cut into
     unsigned long long div_mul;  // division by G
@@ -191,6 +192,7 @@ cudaError_t launch_attention(const AttnParams &p, cudaStream_t s);
 cudaError_t launch_attention_tc(const AttnParams &p, int64_t R, cudaStream_t s);  // cudaErrorNotSupported outside its case
 cudaError_t launch_append(const AppendParams &p, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s);
+cudaError_t launch_prefill_selftest(const PrefillParams &p, cudaStream_t s);
 size_t prefill_scratch_bytes(int64_t L, int64_t S, int64_t H, int64_t G, int D, int64_t T);
 size_t prefill_scratch_most(int64_t L, int64_t H, int64_t G, int D, int64_t T);
 cudaError_t launch_calib_update(const CalibUpdateParams &p, cudaStream_t s);

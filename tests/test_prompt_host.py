@@ -195,3 +195,13 @@ def test_prefill_workspace_of_one_call():
     assert prefill(kv_=kv(n_seqs=1), T=8192, K=None, ws_bytes=256) == BAD
     assert prefill(kv_=kv(n_seqs=1), T=1, K=None, ws_bytes=256) == SMALL
     assert prefill(kv_=kv(n_seqs=1), T=1 << 62, K=None, ws_bytes=256) == BAD
+
+
+def test_prefill_selftest_rejects_bad_arguments():
+    def f(tries, d=64, ws_bytes=1 << 40, K=A):
+        m = tri.model(1, 32, 8, 1e6, head_dim=d)
+        return _abi.load().tri_selftest_prefill_timeout(ctypes.byref(m), ctypes.byref(kv()), K, 2 * A, 3 * A, A, 4, 0.1, 5 * A, None,
+                                                        A, ws_bytes, tries, None)
+
+    assert f(0) == BAD and f((1 << 26) + 1) == BAD and f(9, K=None) == BAD
+    assert f(9, d=128) == UNSUP and f(9, ws_bytes=255) == SMALL
