@@ -109,7 +109,7 @@ def kv_contig(n_seqs: int, row_off: torch.Tensor, total_keys: int,
     """Rows laid end to end; ``row_off`` int64 [R+1] on the device."""
     d = TriKvDesc(TRI_KV_CONTIG, n_seqs, int(total_keys), _p(row_off).value, None, 0, 0, 0,
                   int(elem_type), 0)
-    d._keep = (row_off,)
+    d._keep, d._held = (row_off,), (row_off.numel(), n_seqs, row_off.get_device())
     return d
 
 
@@ -119,7 +119,9 @@ def kv_paged(n_seqs: int, row_off: torch.Tensor, total_keys: int, block_table: t
     d = TriKvDesc(TRI_KV_PAGED, n_seqs, int(total_keys), _p(row_off).value,
                   _p(block_table).value, block_table.shape[1], block_size, int(n_blocks),
                   int(elem_type), 0)
-    d._keep = (row_off, block_table)
+    if row_off.device != block_table.device:
+        raise ValueError("kv_paged: row_off and block_table on different devices")
+    d._keep, d._held = (row_off, block_table), (row_off.numel(), block_table.shape[0], row_off.get_device())
     return d
 
 
@@ -294,8 +296,17 @@ def _arg(t, dev: int, dtype=None, n: int = -1, what: str = ""):
     return t.data_ptr()
 
 
-def _slots(kv: TriKvDesc, m: TriModel) -> int:
-    """Records (a head's key or value of one slot) of the cache ``kv`` describes."""
+def _slots(kv: TriKvDesc, m: TriModel, dev: int) -> int:
+    """Records (a head's key or value of one slot) of the cache ``kv`` describes, whose row offsets and block table
+    are on ``dev`` and reach as far as the kernels read."""
+    held = getattr(kv, "_held", None)  # (a descriptor made by hand has none)
+    if held is not None:
+        offsets, tables, on = held
+        if offsets <= m.n_layers * kv.n_seqs * m.n_kv_heads or tables < kv.n_seqs:
+            raise ValueError(f"kv: {offsets} row offsets and {tables} block tables for {m.n_layers} layers, {kv.n_seqs} "
+                             f"sequences and {m.n_kv_heads} KV heads")
+        if on != dev:
+            raise ValueError(f"kv: descriptor on cuda:{on} in a call on cuda:{dev} (use torch.cuda.device)")
     if kv.layout == TRI_KV_PAGED:
         return m.n_layers * kv.n_blocks * kv.block_size * m.n_kv_heads
     return kv.total_keys
@@ -331,7 +342,7 @@ def tri_append(m: TriModel, kv: TriKvDesc, tokens: TriTokenDesc, key_mode: int, 
         raise ValueError("tokens do not match the model's layers, heads and head dim")
     if tok_off.numel() != kv.n_seqs + 1:
         raise ValueError(f"tok_off: {tok_off.numel()} offsets for {kv.n_seqs} sequences (expected one more)")
-    slots = _slots(kv, m)
+    slots = _slots(kv, m, dev)
     if pos is not None and pos.numel() < slots:
         raise ValueError(f"pos: {pos.numel()} positions for the {slots} records that the descriptor says")
     if k.get_device() != dev:
@@ -360,7 +371,7 @@ def _prefill_args(m, kv, K, V, q, tok_off, softmax_scale, out, lse, ws):
     dev = torch.cuda.current_device()
     heads, d = m.n_layers * m.n_q_heads, m.head_dim
     T = q.numel() // (heads * d)
-    slots = _slots(kv, m)
+    slots = _slots(kv, m, dev)
     return (ctypes.byref(m), ctypes.byref(kv), _cache(K, slots, kv, m, dev, "K"), _cache(V, slots, kv, m, dev, "V"),
             _arg(q, dev, torch.bfloat16, T * heads * d, "q"), _arg(tok_off, dev, torch.int64, kv.n_seqs + 1, "tok_off"), T,
             float(softmax_scale), _arg(out, dev, torch.bfloat16, T * heads * d, "out"),

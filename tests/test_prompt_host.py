@@ -205,3 +205,44 @@ def test_prefill_selftest_rejects_bad_arguments():
 
     assert f(0) == BAD and f((1 << 26) + 1) == BAD and f(9, K=None) == BAD
     assert f(9, d=128) == UNSUP and f(9, ws_bytes=255) == SMALL
+
+
+@pytest.mark.parametrize("layout", ["contig", "paged"])
+def test_append_and_prefill_refuse_descriptors_of_other_sizes(reached, layout):
+    """Row offsets, block tables and devices are compared with the model's: a descriptor made for fewer layers or heads, or
+    on another device, is refused before the library is called."""
+    reached.tri_prefill_attention = reached.tri_append
+    i64, i32, bf16 = torch.int64, torch.int32, torch.bfloat16
+    S, T, h, d = 3, 5, 2, 64
+    n = 4 * 16 * h * 2
+
+    def calls(offsets, tables=S, device=0):
+        off, tab = _Device(i64, offsets), _Device(i32, tables, 4)
+        off.get_device = tab.get_device = lambda: device
+        off.device = tab.device = torch.device("cuda", device)
+        kv_ = tri.kv_paged(S, off, n, tab, 16, 4) if layout == "paged" else tri.kv_contig(S, off, n)
+        m, ws = tri.model(2, 4, h, 1e4, d), _Device(torch.uint8, 256)
+        K, V, tok = _Device(bf16, n, d), _Device(bf16, n, d), _Device(i64, S + 1)
+        t = tri.tokens(_Device(bf16, 2, T, h, d), _Device(bf16, 2, T, h, d), tok, _Device(i32, T))
+        q = _Device(bf16, 2, T, 4, d)
+        return (lambda: tri.tri_append(m, kv_, t, 0, None, K, V, None, ws),
+                lambda: tri.tri_prefill_attention(m, kv_, K, V, q, tok, 0.1, q, None, ws))
+
+    for call in calls(2 * S * h + 1) + calls(2 * S * h + 9):
+        call()
+    assert reached.n == 4
+    wrong = [dict(offsets=2 * S * h), dict(offsets=S * h + 1), dict(offsets=2 * S * h + 1, device=1)]
+    if layout == "paged":
+        wrong.append(dict(offsets=2 * S * h + 1, tables=2))
+    for kw in wrong:
+        for call in calls(**kw):
+            with pytest.raises(ValueError):
+                call()
+    assert reached.n == 4
+
+
+def test_kv_paged_refuses_tensors_on_two_devices():
+    a, b = _Device(torch.int64, 5), _Device(torch.int32, 1, 4)
+    b.device = torch.device("cuda:1")
+    with pytest.raises(ValueError):
+        tri.kv_paged(1, a, 4, b, 16, 4)
