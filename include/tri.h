@@ -459,7 +459,8 @@ typedef struct {
  * A token without a slot (n_s > N) or with inconsistent offsets sets
  * TRI_FLAG_ROW_OFFSETS, one whose block is out of the pool or table
  * TRI_FLAG_BLOCK_TABLE; its key, value and position are not stored (its query is
- * turned all the same).  Slots that two tokens share (a block listed twice) hold
+ * turned all the same).  Limits (TRI_ERR_UNSUPPORTED beyond): T up to 2^31 - 1, n_layers
+ * * T up to 2^40, 2^20 query heads; token rows within 2^56 elements of the first.  Slots that two tokens share (a block listed twice) hold
  * one of them, unspecified which, element by element.
  */
 tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token_desc *tokens, int32_t key_mode,
@@ -489,7 +490,9 @@ tri_status tri_append(const tri_model *m, const tri_kv_desc *kv, const tri_token
  *              TRI_FLAG_BLOCK_TABLE: that key is skipped; TRI_FLAG_STAGE_TIMEOUT: a
  *              copy or product did not complete within 2 s).  Calls that may run at the
  *              same time (two captured graphs, say) need a workspace each.
- * T * G is limited to 2^31 - 256 (TRI_ERR_UNSUPPORTED beyond).
+ * Limits (TRI_ERR_UNSUPPORTED beyond): T * G up to 2^31 - 256, 2^20 query heads, and
+ * (T * G / 128 + min(n_seqs, T)) * n_layers * n_kv_heads up to 2^25; a cache row of more
+ * than 2^31 - 256 slots is flagged (TRI_FLAG_ROW_OFFSETS) and taken as empty.
  * Scores, softmax statistics and sums are fp32.  The weights enter the product with V
  * as e^{s_j} over an earlier or the present maximum, rounded to bf16 (off by at most
  * 2^-8 of themselves).  Over fp8 caches they are fp16 instead (2^-8 of themselves down to

@@ -10,7 +10,7 @@
 // KV head in token order: a prompt of n tokens is n * G rows, cut into items of up to
 // 256.  One block per SM (12 warps) takes item after item: its first by its place in
 // the grid, the next ones from the blocks that the hardware has not launched yet
-// (cluster launch control), heaviest first, so the grid needs no counter in memory.
+// (cluster launch control), a sequence's heaviest first, so the grid needs no counter in memory.
 //
 // For an item's two 128-row query tiles it computes
 //   S = Q K^T  and  O += P V,  P = 2^(S scale log2(e) - m),
@@ -42,7 +42,10 @@
 //
 // The maximum m a row subtracts is only raised when its weights pass 2^8 (bf16) or 2^14 (fp16),
 // which neither these types nor fp32 mind, so O is rescaled rarely.
-// Statistics and O are fp32; P's rounding to bf16 is the operands' common type.
+// Statistics and O are fp32.  P is rounded to bf16 because a product's operands have one type:
+// half a step per weight, which brings outputs to 2.3e-3 of the 64-bit rule (norm of the difference)
+// where rounding them alone gives 1.7e-3.  Two bf16 parts of P, as the single-token call
+// has them, would double the product with V on the unit that bounds prompts.
 //
 // Keys a row must not see get weight exactly 0, but 0 * NaN is NaN in the product:
 // rows of V outside the cache row are zero-filled, and in the tiles that some row sees
@@ -54,9 +57,9 @@
 // first merges the two (a "twin" item; one token over a 2K row waits on the chain product -
 // softmax - product, not on memory).
 //
-// Measured (one B200): an 8K prompt of 32/8 heads of 128 448 us, 1.23 PFLOP/s, 62% of
-// the tensor pipe's cycles; a 16K one 1.67 ms, 1.32 PFLOP/s; 4 tokens over 27K slots of 32
-// heads 99 us, 4.5 TB/s.  Per pair of query tiles and 128 keys the loop takes 3140 cycles, 2048 of
+// Measured (one B200, 32/8 heads of 128): a 32K prompt 7.5 ms, 1.18 PFLOP/s; 16 ragged prompts of
+// 100 to 4096 tokens 770 us, 0.94 PFLOP/s; 512 tokens over 32K paged slots 279 us; 3 to 5 tokens over
+// 20K to 33K paged slots 104 us, 4.3 TB/s.  Per pair of query tiles and 128 keys the loop takes 3140 cycles, 2048 of
 // them the tensor pipe's: each warpgroup's scores, maximum, weights and products are one chain,
 // and the other warpgroup hides two thirds of it.
 //
